@@ -23,6 +23,8 @@
  * The SiLU(z) output gate, the softplus on delta and its per-channel bias
  * are the conventional Mamba block epilogue/prologue; the pages leave them
  * unspecified and this library takes that standard form.
+ * Beside the scan stand the SSD layer, the gated delta rule and the RMS norms
+ * around such a layer, each with its own layouts below.
  *
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers owned by the caller; the
@@ -383,6 +385,120 @@ ssm_status_t ssm_scan_trap_bwd(const void* u, const void* delta, const float* A,
                                float* ddelta_bias, float* dinitial_state,
                                int64_t batch, int64_t L, int64_t dim, int64_t dstate, ssm_dtype_t dt,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The gated delta rule: the linear-state layer whose write corrects what the
+ * state already holds for a key, behind the same per-head scalar fade as the
+ * SSD layer.  Per batch row (or packed sequence) and head, with the state S
+ * (headdim x dstate, the layout of ssm_ssd_fwd's), a_t = exp(step_t A),
+ * step_t = softplus(delta_t + delta_bias) (or the sum itself when
+ * softplus_flag is 0) and b_t = sigmoid(beta_t) (or beta_t itself when
+ * sigmoid_flag is 0):
+ *     S_t = a_t S_{t-1} + b_t (v_t - a_t S_{t-1} k_t) k_t^T,
+ *     y_t = scale S_t q_t,      S_{-1} = initial_state or 0.
+ * With b_t = 1 and orthogonal keys it is a gated linear attention; the SSD
+ * recurrence is the same without the correction (b_t its step, v its x, k its
+ * B, q its C).  Keys are expected with a norm of about 1 (|b k.k| <= 2 keeps
+ * the state bounded); nothing is normalised here.
+ *   q, k: [batch, L, ngroups, dstate]; v, y: [batch, L, heads, headdim];
+ *   delta, beta: [batch, L, heads] (all of dtype dt); A, delta_bias: [heads]
+ *   fp32; head h reads group h / (heads / ngroups) of q and k (ngroups
+ *   divides heads).  States: [rows, heads, headdim, dstate] fp32, rows =
+ *   batch, or nseq with packed sequences.  initial_state (nullable) may be
+ *   the same buffer as final_state (nullable).
+ *   cu_seqlens (NULL: none), nseq: packed sequences as in ssm_scan_fwd_ex
+ *   (batch 1, nseq + 1 int64 device offsets, 8-byte aligned, clamped into
+ *   [0, L] on the device, a start above its end is an empty sequence, whose
+ *   final state is its initial one).  Sequences must not overlap; rows of y
+ *   that belong to no sequence are left as they were.
+ *   q, k and the states 16-byte aligned, everything else to its element.
+ *   dstate 32, 64, 96, 128, 192 or 256, any headdim; else UNSUPPORTED.
+ *   y must not alias an input.
+ * Plans: long bf16 sequences with dstate <= 128 and headdim a multiple of 16
+ * run in chunks of 64 tokens on the matrix cores; everything else runs token
+ * by token in fp32.  In the chunked plan q, k, v and the state pass through
+ * fp16 pairs hi + lo (22 significant bits; q and k convert exactly), so they
+ * must stay below 65504 in magnitude, and what is smaller than 2^-24 counts
+ * as zero; beyond, the outputs become inf or NaN.  Errors as ssm_ssd_fwd. */
+ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
+                           const void* beta, const float* delta_bias, int softplus_flag, int sigmoid_flag,
+                           float scale, const float* initial_state, const int64_t* cu_seqlens, int64_t nseq,
+                           void* y, float* final_state, int64_t batch, int64_t L, int64_t heads, int64_t headdim,
+                           int64_t ngroups, int64_t dstate, ssm_dtype_t dt, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace ssm_delta_fwd needs (0 where it runs token by
+ * token: workspace may then be NULL).  Returns 0 for arguments the call would
+ * reject. */
+size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int64_t headdim, int64_t ngroups,
+                                    int64_t dstate, int64_t nseq, ssm_dtype_t dt);
+
+/* One decode step of the gated delta rule: one token of ssm_delta_fwd, in
+ * fp32, reading `state` [batch, heads, headdim, dstate] as S_{t-1} and
+ * overwriting it in place.  q, k: [batch, ngroups, dstate]; v, y: [batch,
+ * heads, headdim]; delta, beta: [batch, heads].  state must not alias any
+ * other argument. */
+ssm_status_t ssm_delta_update(float* state, const void* q, const void* k, const void* v, const void* delta,
+                              const float* A, const void* beta, const float* delta_bias, int softplus_flag,
+                              int sigmoid_flag, float scale, void* y, int64_t batch, int64_t heads,
+                              int64_t headdim, int64_t ngroups, int64_t dstate, ssm_dtype_t dt,
+                              hipStream_t stream);
+
+/* The RMS norm behind a layer, over groups of `group` consecutive channels
+ * (a head, a part of the row, or the row: group = dim), with its SiLU gate
+ * (z NULL: none) and weight:
+ *     gate_first_flag 0:  y = w * RMS(x) * SiLU(z)      (the delta layer's)
+ *     gate_first_flag 1:  y = w * RMS(x * SiLU(z))      (Mamba-2's)
+ * with RMS(t) = t / sqrt(mean of t^2 over the group + eps).  x, z, y: [rows,
+ * dim] of dtype dt; weight: fp32 [dim], or [group] shared by all groups when
+ * shared_flag is set.  eps >= 0 and finite.  group divides dim (else
+ * INVALID_ARG) and is at most 8192 (else UNSUPPORTED).  y must not alias an
+ * input.  Pointers aligned to their elements; 16-byte aligned ones (and a
+ * group of whole 16-byte pieces) take the fast path. */
+ssm_status_t ssm_gated_norm_fwd(const void* x, const void* z, const float* weight, int shared_flag,
+                                int gate_first_flag, float eps, void* y, int64_t rows, int64_t dim, int64_t group,
+                                ssm_dtype_t dt, hipStream_t stream);
+
+/* Backward of ssm_gated_norm_fwd for dy [rows, dim]: dx and dz (dtype dt; dz
+ * written when both z and dz are given) and dweight (fp32, weight's shape),
+ * summed over the rows (and groups, when shared) in a fixed order.  No output
+ * may alias an input or another output.  workspace:
+ * ssm_gated_norm_bwd_workspace_size() bytes, 256-byte aligned. */
+ssm_status_t ssm_gated_norm_bwd(const void* x, const void* z, const float* weight, int shared_flag,
+                                int gate_first_flag, float eps, const void* dy, void* dx, void* dz, float* dweight,
+                                int64_t rows, int64_t dim, int64_t group, ssm_dtype_t dt, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+size_t ssm_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, ssm_dtype_t dt);
+
+/* The residual stream between two blocks, in one pass: the norm behind the
+ * block (post_weight NULL: none), the residual scale (scale NULL: 1), the
+ * add, and the norm in front of the next block:
+ *     a = post_weight * RMS(x)   (or x),
+ *     residual_out = residual + scale * a        (residual NULL: zero),
+ *     y = weight * RMS(residual + scale * a)     (before it is rounded).
+ * x, y: [rows, dim] of dtype dt; residual, residual_out: [rows, dim] of dtype
+ * res_dt (fp32 with either dt, or bf16 with bf16; else UNSUPPORTED);
+ * residual_out may be the same buffer as residual; y must not alias anything.
+ * scale, post_weight, weight: fp32 [dim].  dim at most 8192 (else
+ * UNSUPPORTED). */
+ssm_status_t ssm_residual_norm_fwd(const void* x, const void* residual, const float* scale,
+                                   const float* post_weight, const float* weight, float eps, void* y,
+                                   void* residual_out, int64_t rows, int64_t dim, ssm_dtype_t dt,
+                                   ssm_dtype_t res_dt, hipStream_t stream);
+
+/* Backward of ssm_residual_norm_fwd from the stream it left (residual_out),
+ * for dy and dresidual_out (the gradient reaching residual_out, res_dt; NULL:
+ * zero): dx (dt), dresidual (res_dt, nullable: not written), dweight, and
+ * dscale and dpost_weight (fp32; written when both the input and the output
+ * are given), summed over the rows in a fixed order.  dresidual may be the
+ * same buffer as dresidual_out; no other output may alias anything.
+ * workspace: ssm_residual_norm_bwd_workspace_size() bytes, 256-byte aligned. */
+ssm_status_t ssm_residual_norm_bwd(const void* x, const void* residual_out, const float* scale,
+                                   const float* post_weight, const float* weight, float eps, const void* dy,
+                                   const void* dresidual_out, void* dx, void* dresidual, float* dscale,
+                                   float* dpost_weight, float* dweight, int64_t rows, int64_t dim, ssm_dtype_t dt,
+                                   ssm_dtype_t res_dt, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+size_t ssm_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim, ssm_dtype_t dt, ssm_dtype_t res_dt);
 
 /* Outcome of the kernels of the last call that used `workspace` (any entry
  * point taking a workspace): SSM_OK, or SSM_ERR_HANDOFF_TIMEOUT when a chained

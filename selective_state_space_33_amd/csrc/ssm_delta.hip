@@ -1,0 +1,117 @@
+// ssm_delta.hip -- C-ABI entry points of the gated delta rule, forward and
+// one-token step (declared with their contracts in include/ssm_scan.h).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "delta_host.hpp"
+#include "delta_step_kernel.hpp"
+#include "host_common.hpp"
+#include "ssm_scan.h"
+
+namespace ssm {
+namespace {
+
+// Rows of the state per wavefront: 8 RPT.  More rows amortise the keys and
+// queries that every wavefront loads and put more loads in flight; fewer give
+// short batches more wavefronts.
+template <class IO, int DK> hipError_t launch_step(DeltaStepParams& p, int64_t units, hipStream_t s) {
+  constexpr int RPT = DK <= 128 ? 4 : 2;
+  const int64_t wide = kDeltaStepWaves * 8 * RPT, narrow = kDeltaStepWaves * 8;
+  if (units * ((p.P + wide - 1) / wide) >= 2 * device_cu_count()) {
+    p.row_blocks = (p.P + wide - 1) / wide;
+    if (units * p.row_blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((delta_step_kernel<IO, DK, RPT>), dim3(static_cast<unsigned>(units * p.row_blocks)),
+                       dim3(64 * kDeltaStepWaves), 0, s, p);
+  } else {
+    p.row_blocks = (p.P + narrow - 1) / narrow;
+    if (units * p.row_blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((delta_step_kernel<IO, DK, 1>), dim3(static_cast<unsigned>(units * p.row_blocks)),
+                       dim3(64 * kDeltaStepWaves), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+template <class IO> hipError_t run_step(DeltaStepParams& p, int64_t units, int64_t dstate, hipStream_t s) {
+  switch (dstate) {
+    case 32: return launch_step<IO, 32>(p, units, s);
+    case 64: return launch_step<IO, 64>(p, units, s);
+    case 96: return launch_step<IO, 96>(p, units, s);
+    case 128: return launch_step<IO, 128>(p, units, s);
+    case 192: return launch_step<IO, 192>(p, units, s);
+    case 256: return launch_step<IO, 256>(p, units, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+DeltaStepParams step_params(const DeltaArgs& a) {
+  DeltaStepParams p = {};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.delta = a.delta;
+  p.A = a.A;
+  p.beta = a.beta;
+  p.bias = a.bias;
+  p.h0 = a.h0;
+  p.cu = a.cu;
+  p.L = a.L;
+  p.H = a.heads;
+  p.G = a.ngroups;
+  p.P = a.headdim;
+  p.softplus = a.softplus;
+  p.sigmoid = a.sigmoid;
+  p.scale = a.scale;
+  return p;
+}
+
+}  // namespace
+}  // namespace ssm
+
+using namespace ssm;
+
+extern "C" ssm_status_t ssm_delta_update(float* state, const void* q, const void* k, const void* v,
+                                         const void* delta, const float* A, const void* beta,
+                                         const float* delta_bias, int softplus_flag, int sigmoid_flag, float scale,
+                                         void* y, int64_t batch, int64_t heads, int64_t headdim, int64_t ngroups,
+                                         int64_t dstate, ssm_dtype_t dt, hipStream_t stream) {
+  if (!state || !y) return SSM_ERR_INVALID_ARG;
+  const DeltaArgs a = {q,     k,     v, delta, A,     beta,    delta_bias, state,  nullptr, 0,
+                       batch, 1,     heads,    headdim, ngroups, dstate,   softplus_flag ? 1 : 0,
+                       sigmoid_flag ? 1 : 0, scale, dt};
+  const ssm_status_t st = check_delta_args(a, y, state);
+  if (st != SSM_OK) return st;
+  DeltaStepParams p = step_params(a);
+  p.hT = state;
+  p.y = y;
+  const hipError_t e = dt == SSM_DTYPE_F32 ? run_step<F32>(p, batch * heads, dstate, stream)
+                                           : run_step<BF16>(p, batch * heads, dstate, stream);
+  return e == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+extern "C" size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int64_t headdim,
+                                               int64_t ngroups, int64_t dstate, int64_t nseq, ssm_dtype_t dt) {
+  (void)batch, (void)L, (void)heads, (void)headdim, (void)ngroups, (void)dstate, (void)nseq, (void)dt;
+  return 0;
+}
+
+extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
+                                      const void* beta, const float* delta_bias, int softplus_flag,
+                                      int sigmoid_flag, float scale, const float* initial_state,
+                                      const int64_t* cu_seqlens, int64_t nseq, void* y, float* final_state,
+                                      int64_t batch, int64_t L, int64_t heads, int64_t headdim, int64_t ngroups,
+                                      int64_t dstate, ssm_dtype_t dt, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+  const DeltaArgs a = {q,     k, v,     delta,   A,       beta,   delta_bias, initial_state, cu_seqlens, nseq,
+                       batch, L, heads, headdim, ngroups, dstate, softplus_flag ? 1 : 0, sigmoid_flag ? 1 : 0,
+                       scale, dt};
+  const ssm_status_t st = check_delta_args(a, y, final_state);
+  if (st != SSM_OK) return st;
+  (void)workspace, (void)workspace_bytes;
+  DeltaStepParams p = step_params(a);
+  p.hT = final_state;
+  p.y = y;
+  const int64_t units = (cu_seqlens ? nseq : batch) * heads;
+  const hipError_t e = dt == SSM_DTYPE_F32 ? run_step<F32>(p, units, dstate, stream)
+                                           : run_step<BF16>(p, units, dstate, stream);
+  return e == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}

@@ -202,3 +202,21 @@ def random_ssd_inputs(rng: np.random.Generator, batch: int, L: int, heads: int, 
         "B": _store(B, dtype), "C": _store(C, dtype), "A": A, "D": np.ones(heads, dtype=np.float32),
         "delta_bias": bias,
     }
+
+
+def random_delta_inputs(rng: np.random.Generator, batch: int, L: int, ngroups: int, heads: int, dstate: int,
+                        headdim: int, dtype: str = "bf16") -> dict:
+    """Seeded inputs of the gated delta rule (float32 arrays, bf16-representable where stored as bf16).
+
+    q, k: [batch, L, ngroups, dstate] = SiLU(N(0, 1)) with unit norm (what a short convolution and an L2 norm leave);
+    v: [batch, L, heads, headdim] = SiLU(N(0, 1)); delta, beta (raw): [batch, L, heads] ~ N(0, 1); A: [heads] =
+    -U[1, 16]; delta_bias = log(expm1(U[1e-3, 0.1]))."""
+    silu = lambda x: x / (1.0 + np.exp(-x))  # noqa: E731
+    unit = lambda x: x / np.maximum(np.linalg.norm(x, axis=-1, keepdims=True), 1e-6)  # noqa: E731
+    n = lambda *shape: rng.standard_normal(shape)  # noqa: E731
+    q, k = (_store(unit(silu(n(batch, L, ngroups, dstate))), dtype) for _ in range(2))
+    v = _store(silu(n(batch, L, heads, headdim)), dtype)
+    delta, beta = (_store(n(batch, L, heads), dtype) for _ in range(2))
+    A = -rng.uniform(1.0, 16.0, heads).astype(np.float32)
+    bias = np.log(np.expm1(rng.uniform(1e-3, 0.1, heads))).astype(np.float32)
+    return dict(q=q, k=k, v=v, delta=delta, A=A, beta=beta, delta_bias=bias)

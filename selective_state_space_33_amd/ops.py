@@ -35,6 +35,9 @@ EXPORTED = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_noalloc", "
             "ssm_scan_trap_fwd_workspace_size", "ssm_scan_trap_fwd", "ssm_ssd_fwd_workspace_size", "ssm_ssd_fwd",
             "ssm_state_update",
             "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_scan_trap_bwd_workspace_size", "ssm_scan_trap_bwd",
+            "ssm_delta_fwd_workspace_size", "ssm_delta_fwd", "ssm_delta_update",
+            "ssm_gated_norm_fwd", "ssm_gated_norm_bwd_workspace_size", "ssm_gated_norm_bwd",
+            "ssm_residual_norm_fwd", "ssm_residual_norm_bwd_workspace_size", "ssm_residual_norm_bwd",
             "ssm_workspace_status", "ssm_status_string")
 
 _lib = None
@@ -91,6 +94,28 @@ def lib() -> ctypes.CDLL:
                                          [ctypes.c_int, _vp, ctypes.c_size_t, _vp])
         L.ssm_scan_trap_bwd_workspace_size.restype = ctypes.c_size_t
         L.ssm_scan_trap_bwd_workspace_size.argtypes = [_i64] * 5 + [ctypes.c_int]
+        _int, _flt, _size = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        L.ssm_delta_fwd_workspace_size.restype = _size
+        L.ssm_delta_fwd_workspace_size.argtypes = [_i64] * 7 + [_int]
+        L.ssm_delta_fwd.restype = _int
+        L.ssm_delta_fwd.argtypes = ([_vp] * 7 + [_int, _int, _flt, _vp, _vp, _i64, _vp, _vp] + [_i64] * 6 +
+                                    [_int, _vp, _size, _vp])
+        L.ssm_delta_update.restype = _int
+        L.ssm_delta_update.argtypes = [_vp] * 8 + [_int, _int, _flt, _vp] + [_i64] * 5 + [_int, _vp]
+        L.ssm_gated_norm_fwd.restype = _int
+        L.ssm_gated_norm_fwd.argtypes = [_vp] * 3 + [_int, _int, _flt, _vp] + [_i64] * 3 + [_int, _vp]
+        L.ssm_gated_norm_bwd_workspace_size.restype = _size
+        L.ssm_gated_norm_bwd_workspace_size.argtypes = [_i64] * 3 + [_int]
+        L.ssm_gated_norm_bwd.restype = _int
+        L.ssm_gated_norm_bwd.argtypes = ([_vp] * 3 + [_int, _int, _flt] + [_vp] * 4 + [_i64] * 3 +
+                                         [_int, _vp, _size, _vp])
+        L.ssm_residual_norm_fwd.restype = _int
+        L.ssm_residual_norm_fwd.argtypes = [_vp] * 5 + [_flt, _vp, _vp, _i64, _i64, _int, _int, _vp]
+        L.ssm_residual_norm_bwd_workspace_size.restype = _size
+        L.ssm_residual_norm_bwd_workspace_size.argtypes = [_i64] * 2 + [_int] * 2
+        L.ssm_residual_norm_bwd.restype = _int
+        L.ssm_residual_norm_bwd.argtypes = ([_vp] * 5 + [_flt] + [_vp] * 7 + [_i64] * 2 +
+                                            [_int, _int, _vp, _size, _vp])
         L.ssm_workspace_status.restype = ctypes.c_int
         L.ssm_workspace_status.argtypes = [_vp, ctypes.c_size_t, _vp]
         L.ssm_status_string.restype = ctypes.c_char_p
@@ -457,4 +482,222 @@ def ssm_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, softplu
         raise SSMError(rc, name)
     if check_status:
         _check_status(workspace, s, name)
+    return g
+
+
+def _delta_args(q, k, v, delta, A, beta, delta_bias, initial_state, cu_seqlens):
+    """Checks the gated delta rule's tensors; returns (batch, L, heads, headdim, ngroups, dstate, nseq, rows)."""
+    batch, L, heads, headdim = v.shape
+    ngroups, dstate = k.shape[2], k.shape[3]
+    dev, dt = v.device, v.dtype
+    nseq, rows = 0, batch
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int64 or cu_seqlens.device != dev or cu_seqlens.dim() != 1:
+            raise TypeError("cu_seqlens must be a 1-d int64 tensor on the device of v")
+        nseq = rows = cu_seqlens.numel() - 1
+        _check(cu_seqlens, "cu_seqlens", torch.int64, (nseq + 1,), dev)
+    for name, t, shp in (("q", q, (batch, L, ngroups, dstate)), ("k", k, (batch, L, ngroups, dstate)),
+                         ("v", v, (batch, L, heads, headdim)), ("delta", delta, (batch, L, heads)),
+                         ("beta", beta, (batch, L, heads))):
+        _check(t, name, dt, shp, dev)
+    _check(A, "A", torch.float32, (heads,), dev)
+    _check(delta_bias, "delta_bias", torch.float32, (heads,), dev)
+    _check(initial_state, "initial_state", torch.float32, (rows, heads, headdim, dstate), dev)
+    return batch, L, heads, headdim, ngroups, dstate, nseq, rows
+
+
+def ssm_delta_fwd_workspace_size(batch: int, L: int, heads: int, headdim: int, ngroups: int, dstate: int, nseq: int,
+                                 dtype: torch.dtype) -> int:
+    return int(lib().ssm_delta_fwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq,
+                                                  _dtype_code(dtype)))
+
+
+def ssm_delta_fwd(q, k, v, delta, A, beta, delta_bias=None, softplus: bool = True, sigmoid: bool = True,
+                  scale: Optional[float] = None, initial_state=None, cu_seqlens=None, y=None, final_state=None,
+                  return_final_state: bool = True, workspace=None, stream=None):
+    """The gated delta rule over whole sequences: S <- a S + b (v - a S k) k^T, y = scale S q with
+    a = exp(softplus(delta + delta_bias) A) and b = sigmoid(beta).
+
+    q, k: [batch, L, ngroups, dstate]; v: [batch, L, heads, headdim]; delta, beta: [batch, L, heads] (bfloat16 or
+    float32, all the same; heads a multiple of ngroups); A, delta_bias: [heads] (float32).  scale: 1/sqrt(dstate)
+    if None.  initial_state: [rows, heads, headdim, dstate] (float32) or None; cu_seqlens: int64 device tensor of
+    nseq + 1 offsets into the L axis of batch row 0 (rows = nseq; otherwise rows = batch).
+    Returns (y [batch, L, heads, headdim], final_state [rows, heads, headdim, dstate] or None)."""
+    batch, L, heads, headdim, ngroups, dstate, nseq, rows = _delta_args(q, k, v, delta, A, beta, delta_bias,
+                                                                        initial_state, cu_seqlens)
+    dev, dt = v.device, v.dtype
+    code = _dtype_code(dt)
+    s = _resolve(dev, stream)
+    with torch.cuda.stream(s):
+        if y is None:
+            y = torch.empty_like(v)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((rows, heads, headdim, dstate), dtype=torch.float32, device=dev)
+        need = ssm_delta_fwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq, dt)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(y, "y", dt, (batch, L, heads, headdim), dev)
+    _check(final_state, "final_state", torch.float32, (rows, heads, headdim, dstate), dev)
+    rc = lib().ssm_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta), _ptr(delta_bias),
+                             1 if softplus else 0, 1 if sigmoid else 0, dstate ** -0.5 if scale is None else scale,
+                             _ptr(initial_state), _ptr(cu_seqlens), nseq, _ptr(y), _ptr(final_state), batch, L,
+                             heads, headdim, ngroups, dstate, code, _ptr(workspace), _ws_bytes(workspace),
+                             s.cuda_stream)
+    if rc != SSM_OK:
+        raise SSMError(rc, "ssm_delta_fwd")
+    return y, final_state
+
+
+def ssm_delta_update(state, q, k, v, delta, A, beta, delta_bias=None, softplus: bool = True, sigmoid: bool = True,
+                     scale: Optional[float] = None, y=None, stream=None):
+    """One decode step of the gated delta rule; `state` [batch, heads, headdim, dstate] (float32) is updated in place.
+
+    q, k: [batch, ngroups, dstate]; v: [batch, heads, headdim]; delta, beta: [batch, heads]; the rest as
+    ssm_delta_fwd.  Returns y [batch, heads, headdim]."""
+    batch, heads, headdim = v.shape
+    ngroups, dstate = k.shape[1], k.shape[2]
+    dev, dt = v.device, v.dtype
+    code = _dtype_code(dt)
+    _check(state, "state", torch.float32, (batch, heads, headdim, dstate), dev)
+    for name, t, shp in (("q", q, (batch, ngroups, dstate)), ("k", k, (batch, ngroups, dstate)),
+                         ("v", v, (batch, heads, headdim)), ("delta", delta, (batch, heads)),
+                         ("beta", beta, (batch, heads))):
+        _check(t, name, dt, shp, dev)
+    _check(A, "A", torch.float32, (heads,), dev)
+    _check(delta_bias, "delta_bias", torch.float32, (heads,), dev)
+    s = _resolve(dev, stream)
+    if y is None:
+        with torch.cuda.stream(s):
+            y = torch.empty_like(v)
+    _check(y, "y", dt, (batch, heads, headdim), dev)
+    rc = lib().ssm_delta_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta),
+                                _ptr(delta_bias), 1 if softplus else 0, 1 if sigmoid else 0,
+                                dstate ** -0.5 if scale is None else scale, _ptr(y), batch, heads, headdim, ngroups,
+                                dstate, code, s.cuda_stream)
+    if rc != SSM_OK:
+        raise SSMError(rc, "ssm_delta_update")
+    return y
+
+
+def _gated_args(x, z, weight, group):
+    """Checks the gated norm's tensors; returns (rows, dim, group, shared)."""
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    group = dim if group is None else group
+    _check(x, "x", x.dtype, x.shape, x.device)
+    _check(z, "z", x.dtype, x.shape, x.device)
+    shared = weight.numel() != dim
+    _check(weight, "weight", torch.float32, (group if shared else dim,), x.device)
+    return rows, dim, group, 1 if shared else 0
+
+
+def ssm_gated_norm_fwd(x, z, weight, group: Optional[int] = None, eps: float = 1e-5, gate_first: bool = False,
+                       y=None, stream=None):
+    """The RMS norm behind a layer with its gate: weight * RMS(x) * SiLU(z), or with gate_first
+    weight * RMS(x * SiLU(z)), over groups of `group` channels (None: the whole last axis).
+
+    x, z: [..., dim] (bfloat16 or float32; z may be None); weight: [dim], or [group] shared by the groups (float32).
+    Returns y like x."""
+    rows, dim, group, shared = _gated_args(x, z, weight, group)
+    code = _dtype_code(x.dtype)
+    s = _resolve(x.device, stream)
+    if y is None:
+        with torch.cuda.stream(s):
+            y = torch.empty_like(x)
+    _check(y, "y", x.dtype, x.shape, x.device)
+    rc = lib().ssm_gated_norm_fwd(_ptr(x), _ptr(z), _ptr(weight), shared, 1 if gate_first else 0, eps, _ptr(y), rows,
+                                  dim, group, code, s.cuda_stream)
+    if rc != SSM_OK:
+        raise SSMError(rc, "ssm_gated_norm_fwd")
+    return y
+
+
+def ssm_gated_norm_bwd_workspace_size(rows: int, dim: int, group: int, dtype: torch.dtype) -> int:
+    return int(lib().ssm_gated_norm_bwd_workspace_size(rows, dim, group, _dtype_code(dtype)))
+
+
+def ssm_gated_norm_bwd(x, z, weight, dy, group: Optional[int] = None, eps: float = 1e-5, gate_first: bool = False,
+                       workspace=None, stream=None):
+    """Backward of ssm_gated_norm_fwd: a dict of dx, dz (None without z) and dweight (float32, weight's shape)."""
+    rows, dim, group, shared = _gated_args(x, z, weight, group)
+    dev, code = x.device, _dtype_code(x.dtype)
+    _check(dy, "dy", x.dtype, x.shape, dev)
+    s = _resolve(dev, stream)
+    with torch.cuda.stream(s):
+        g = dict(dx=torch.empty_like(x), dz=None if z is None else torch.empty_like(z),
+                 dweight=torch.empty_like(weight))
+        need = int(lib().ssm_gated_norm_bwd_workspace_size(rows, dim, group, code))
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = lib().ssm_gated_norm_bwd(_ptr(x), _ptr(z), _ptr(weight), shared, 1 if gate_first else 0, eps, _ptr(dy),
+                                  _ptr(g["dx"]), _ptr(g["dz"]), _ptr(g["dweight"]), rows, dim, group, code,
+                                  _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
+    if rc != SSM_OK:
+        raise SSMError(rc, "ssm_gated_norm_bwd")
+    return g
+
+
+def _residual_args(x, residual, weight, scale, post_weight):
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    _check(x, "x", x.dtype, x.shape, x.device)
+    if residual is not None:
+        _check(residual, "residual", residual.dtype, x.shape, x.device)
+    for name, t in (("weight", weight), ("scale", scale), ("post_weight", post_weight)):
+        _check(t, name, torch.float32, (dim,), x.device)
+    return rows, dim
+
+
+def ssm_residual_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps: float = 1e-5, y=None,
+                          residual_out=None, stream=None):
+    """The residual stream between two blocks: r = residual + scale * (post_weight * RMS(x), or x), y = weight * RMS(r).
+
+    x: [..., dim] (bfloat16 or float32); residual: the same shape (float32, or bfloat16 with a bfloat16 x), None for
+    zero; weight, scale, post_weight: [dim] (float32).  residual_out may be residual itself; without a residual it
+    defaults to float32.  Returns (y like x, residual_out)."""
+    rows, dim = _residual_args(x, residual, weight, scale, post_weight)
+    dev, code = x.device, _dtype_code(x.dtype)
+    s = _resolve(dev, stream)
+    with torch.cuda.stream(s):
+        if y is None:
+            y = torch.empty_like(x)
+        if residual_out is None:
+            residual_out = torch.empty_like(x if residual is None else residual,
+                                            dtype=torch.float32 if residual is None else residual.dtype)
+    _check(y, "y", x.dtype, x.shape, dev)
+    _check(residual_out, "residual_out", residual_out.dtype if residual is None else residual.dtype, x.shape, dev)
+    rc = lib().ssm_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(scale), _ptr(post_weight), _ptr(weight), eps,
+                                     _ptr(y), _ptr(residual_out), rows, dim, code, _dtype_code(residual_out.dtype),
+                                     s.cuda_stream)
+    if rc != SSM_OK:
+        raise SSMError(rc, "ssm_residual_norm_fwd")
+    return y, residual_out
+
+
+def ssm_residual_norm_bwd_workspace_size(rows: int, dim: int, dtype: torch.dtype, res_dtype: torch.dtype) -> int:
+    return int(lib().ssm_residual_norm_bwd_workspace_size(rows, dim, _dtype_code(dtype), _dtype_code(res_dtype)))
+
+
+def ssm_residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, scale=None, post_weight=None,
+                          eps: float = 1e-5, want_dresidual: bool = True, workspace=None, stream=None):
+    """Backward of ssm_residual_norm_fwd from the stream it left (residual_out): a dict of dx, dresidual (None
+    unless wanted), dweight, and dscale and dpost_weight for the inputs given (None otherwise)."""
+    rows, dim = _residual_args(x, residual_out, weight, scale, post_weight)
+    dev, code, rcode = x.device, _dtype_code(x.dtype), _dtype_code(residual_out.dtype)
+    _check(dy, "dy", x.dtype, x.shape, dev)
+    _check(dresidual_out, "dresidual_out", residual_out.dtype, x.shape, dev)
+    s = _resolve(dev, stream)
+    with torch.cuda.stream(s):
+        g = dict(dx=torch.empty_like(x), dresidual=torch.empty_like(residual_out) if want_dresidual else None,
+                 dweight=torch.empty_like(weight), dscale=None if scale is None else torch.empty_like(scale),
+                 dpost_weight=None if post_weight is None else torch.empty_like(post_weight))
+        need = int(lib().ssm_residual_norm_bwd_workspace_size(rows, dim, code, rcode))
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = lib().ssm_residual_norm_bwd(_ptr(x), _ptr(residual_out), _ptr(scale), _ptr(post_weight), _ptr(weight), eps,
+                                     _ptr(dy), _ptr(dresidual_out), _ptr(g["dx"]), _ptr(g["dresidual"]),
+                                     _ptr(g["dscale"]), _ptr(g["dpost_weight"]), _ptr(g["dweight"]), rows, dim, code,
+                                     rcode, _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
+    if rc != SSM_OK:
+        raise SSMError(rc, "ssm_residual_norm_bwd")
     return g

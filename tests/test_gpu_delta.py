@@ -1,0 +1,223 @@
+"""GPU parity of the gated delta rule (ssm_delta_fwd, ssm_delta_update) against its fp64 oracle (oracle/delta.py).
+
+Error measure: that of gpu_util (|g - o| over max(|o|, rms(o)), the largest).  Tolerances, derived beforehand:
+  - fp32 arithmetic, token by token: a token adds a product of up to 256 terms for r and one for y, rounded at
+    2^-24 of the terms' magnitudes each; with unit keys and a fading state the errors of earlier tokens fade too.
+    256 x 2^-24 = 1.5e-5, twice that for r's way through the state: 3e-5, for y and the state.
+  - the chunked plan keeps 22 significant bits on the state's path: three products a chunk, each off by 2 x 2^-22 of
+    its terms, below the same 3e-5 for the state.  y takes the state, u and the scores rounded to fp16 once
+    (2^-11 each): sums of many such terms with independent roundings stay below 3 x 2^-11 x rms = 1.5e-3.
+  - y in bf16 adds half a step, 2^-8.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import delta as D
+from selective_state_space_33_amd import inputs as I
+from selective_state_space_33_amd import ops
+
+from .gpu_util import rel_err, say
+
+pytestmark = pytest.mark.gpu
+
+TOL_STATE = 3e-5
+TOL_Y = {"f32": 3e-5, "bf16": 2.0 ** -8 + 1.5e-3}
+
+
+def dev(a, dtype="f32"):
+    if a is None:
+        return None
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to("cuda:0")
+    return t.to(torch.bfloat16) if dtype == "bf16" else t
+
+
+def tensors(x, dtype):
+    return {n: dev(a, "f32" if n in ("A", "delta_bias") else dtype) for n, a in x.items()}
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def run(x, dtype, h0=None, cu=None, **kw):
+    t = tensors(x, dtype)
+    y, s = ops.ssm_delta_fwd(t["q"], t["k"], t["v"], t["delta"], t["A"], t["beta"], delta_bias=t["delta_bias"],
+                             initial_state=dev(h0),
+                             cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int64, device="cuda:0"),
+                             **kw)
+    torch.cuda.synchronize()
+    return y, s
+
+
+def check(x, dtype, label, h0=None, cu=None, **kw):
+    say(f"delta {label} q={x['q'].shape} v={x['v'].shape} {dtype}")
+    # rows of no sequence are not written: they hold the zeros that the oracle has there
+    y, s = run(x, dtype, h0, cu, y=dev(np.zeros(x["v"].shape), dtype), **kw)
+    yo, so = D.delta_fwd(**x, initial_state=h0, cu_seqlens=cu, **kw)
+    ey, es = rel_err(host(y), yo), rel_err(host(s), so)
+    print(f"[parity] delta {label}: y {ey:.2e} state {es:.2e}", flush=True)
+    assert ey <= TOL_Y[dtype] and es <= TOL_STATE, (ey, es)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,P", [(32, 16), (64, 64), (96, 48), (128, 128), (192, 32), (256, 64), (64, 37), (128, 3)])
+def test_forward_shapes(N, P, dtype):
+    x = I.random_delta_inputs(np.random.default_rng(1000 + N + P), 2, 75, 2, 4, N, P, dtype)
+    check(x, dtype, f"N={N} P={P}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [1, 2, 15, 63, 64, 65, 127, 128, 129, 200, 321])
+def test_forward_lengths(L, dtype):
+    rng = np.random.default_rng(1100 + L)
+    x = I.random_delta_inputs(rng, 3, L, 3, 6, 64, 32, dtype)
+    check(x, dtype, f"L={L}", h0=0.3 * rng.standard_normal((3, 6, 32, 64)).astype(np.float32))
+
+
+@pytest.mark.parametrize("L", [70, 500])
+@pytest.mark.parametrize("opts", ["plain", "no_bias", "no_softplus", "no_sigmoid", "beta_zero", "beta_two", "scale"])
+def test_forward_options(opts, L):
+    rng = np.random.default_rng(1200 + len(opts) + L)
+    x = I.random_delta_inputs(rng, 2, L, 2, 2, 128, 64)
+    kw = {}
+    if opts == "no_bias":
+        x["delta_bias"] = None
+    elif opts == "no_softplus":
+        kw["softplus"] = False
+        x["delta"] = I.round_to_bf16(np.abs(x["delta"]) * 0.05 + 0.01)  # the step itself: keep it positive
+        x["delta_bias"] = np.abs(x["delta_bias"]) * 0.01
+    elif opts in ("no_sigmoid", "beta_zero", "beta_two"):
+        kw["sigmoid"] = False
+        b = {"no_sigmoid": rng.random(x["beta"].shape), "beta_zero": np.zeros(x["beta"].shape),
+             "beta_two": np.full(x["beta"].shape, 1.9375)}[opts]
+        x["beta"] = I.round_to_bf16(b.astype(np.float32))
+    elif opts == "scale":
+        kw["scale"] = 1.75
+    check(x, "bf16", f"{opts} L={L}", h0=rng.standard_normal((2, 2, 64, 128)).astype(np.float32), **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_packed_sequences(dtype):
+    """Lengths of zero, one, a chunk and more, from given states; the tokens behind the last sequence and their y stay."""
+    rng = np.random.default_rng(1300)
+    lens = [70, 0, 1, 64, 130, 0, 17, 65]
+    L = sum(lens) + 9
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    x = I.random_delta_inputs(rng, 1, L, 2, 4, 64, 48, dtype)
+    h0 = 0.5 * rng.standard_normal((len(lens), 4, 48, 64)).astype(np.float32)
+    say(f"delta packed {dtype}")
+    y0 = dev(np.full(x["v"].shape, 7.0), dtype)
+    y, s = run(x, dtype, h0, cu, y=y0)
+    yo, so = D.delta_fwd(**x, initial_state=h0, cu_seqlens=cu, y_before=np.full(x["v"].shape, 7.0))
+    assert torch.equal(y[:, cu[-1]:], torch.full_like(y[:, cu[-1]:], 7.0))
+    assert np.array_equal(host(s)[[1, 5]], h0[[1, 5]].astype(np.float64))
+    ey, es = rel_err(host(y), yo), rel_err(host(s), so)
+    print(f"[parity] delta packed {dtype}: y {ey:.2e} state {es:.2e}", flush=True)
+    assert ey <= TOL_Y[dtype] and es <= TOL_STATE
+
+
+def test_packed_offsets_outside_the_row_are_clamped():
+    rng = np.random.default_rng(1310)
+    x = I.random_delta_inputs(rng, 1, 150, 1, 2, 32, 32)
+    check(x, "bf16", "clamped offsets", cu=[-5, 80, 400])
+    check(x, "bf16", "an offset that goes back", cu=[0, 90, 40])
+
+
+def test_extreme_steps_and_fades():
+    """Raw steps spread over +-60: fades that underflow to 0 within a chunk next to ones that stay at 1."""
+    rng = np.random.default_rng(1320)
+    x = I.random_delta_inputs(rng, 2, 200, 2, 4, 64, 64)
+    x["delta"] = I.round_to_bf16(x["delta"].astype(np.float64) * 20.0)
+    check(x, "bf16", "extreme steps", h0=rng.standard_normal((2, 4, 64, 64)).astype(np.float32))
+
+
+def test_repeated_keys():
+    """The same key at every token (the chunk's triangular system at its worst): each write replaces the last one."""
+    rng = np.random.default_rng(1330)
+    x = I.random_delta_inputs(rng, 1, 190, 1, 2, 64, 32)
+    x["k"][:] = x["k"][:, :1]
+    x["delta_bias"] = np.full(2, -20.0, np.float32)     # hardly any fade
+    x["delta"][:] = 0.0
+    x["beta"] = I.round_to_bf16(np.full(x["beta"].shape, 1.0, np.float32))
+    check(x, "bf16", "repeated keys", sigmoid=False)
+
+
+def test_nan_stays_in_its_head_and_behind_its_token():
+    rng = np.random.default_rng(1340)
+    x = I.random_delta_inputs(rng, 2, 140, 2, 4, 64, 32)
+    x["v"][1, 70, 2, 5] = np.nan
+    say("delta NaN")
+    y, s = run(x, "bf16")
+    bad = ~np.isfinite(host(y))
+    assert bad[1, 70:, 2, 5].all()
+    bad[1, 70:, 2, 5] = False
+    # a chunk's other tokens of that channel may share its products, nothing else does
+    bad[1, 64:70, 2, 5] = False
+    assert not bad.any()
+    sb = ~np.isfinite(host(s))
+    assert sb[1, 2, 5].all() and sb.sum() == 64
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,G,H,N,P", [(1, 1, 1, 32, 16), (5, 2, 6, 64, 64), (33, 20, 40, 128, 128), (3, 1, 2, 96, 50),
+                                           (2, 2, 2, 256, 70), (1, 4, 4, 192, 1)])
+def test_step_against_oracle(batch, G, H, N, P, dtype):
+    rng = np.random.default_rng(1400 + N + P)
+    x = I.random_delta_inputs(rng, batch, 1, G, H, N, P, dtype)
+    h0 = rng.standard_normal((batch, H, P, N)).astype(np.float32)
+    say(f"delta step {batch}x{G}/{H}x{N}x{P} {dtype}")
+    t = tensors(x, dtype)
+    state = dev(h0)
+    one = lambda a: a[:, 0].contiguous()  # noqa: E731
+    y = ops.ssm_delta_update(state, one(t["q"]), one(t["k"]), one(t["v"]), one(t["delta"]), t["A"], one(t["beta"]),
+                             delta_bias=t["delta_bias"])
+    torch.cuda.synchronize()
+    yo, so = D.delta_fwd(**x, initial_state=h0)
+    ey, es = rel_err(host(y), yo[:, 0]), rel_err(host(state), so)
+    print(f"[parity] delta step: y {ey:.2e} state {es:.2e}", flush=True)
+    assert ey <= TOL_Y[dtype] and es <= TOL_STATE
+
+
+def test_steps_continue_a_prefill():
+    """A prompt through ssm_delta_fwd, then tokens one by one from its final state: the same as all of it at once."""
+    rng = np.random.default_rng(1500)
+    x = I.random_delta_inputs(rng, 2, 150, 2, 4, 128, 64)
+    h0 = rng.standard_normal((2, 4, 64, 128)).astype(np.float32)
+    say("delta prefill then steps")
+    t = tensors(x, "bf16")
+    cut = 145
+    part = lambda a: a[:, :cut].contiguous()  # noqa: E731
+    _, state = ops.ssm_delta_fwd(part(t["q"]), part(t["k"]), part(t["v"]), part(t["delta"]), t["A"], part(t["beta"]),
+                                 delta_bias=t["delta_bias"], initial_state=dev(h0))
+    ys = []
+    for i in range(cut, 150):
+        one = lambda a: a[:, i].contiguous()  # noqa: E731,B023
+        ys.append(ops.ssm_delta_update(state, one(t["q"]), one(t["k"]), one(t["v"]), one(t["delta"]), t["A"],
+                                       one(t["beta"]), delta_bias=t["delta_bias"]))
+    torch.cuda.synchronize()
+    yo, so = D.delta_fwd(**x, initial_state=h0)
+    ey, es = rel_err(np.stack([host(y) for y in ys], 1), yo[:, cut:]), rel_err(host(state), so)
+    print(f"[parity] delta prefill then steps: y {ey:.2e} state {es:.2e}", flush=True)
+    assert ey <= TOL_Y["bf16"] and es <= TOL_STATE
+
+
+def test_final_state_in_the_initial_states_buffer_and_determinism():
+    rng = np.random.default_rng(1510)
+    x = I.random_delta_inputs(rng, 2, 300, 2, 4, 128, 64)
+    h0 = rng.standard_normal((2, 4, 64, 128)).astype(np.float32)
+    say("delta in place")
+    y1, s1 = run(x, "bf16", h0)
+    t, state = tensors(x, "bf16"), dev(h0)
+    y2, s2 = ops.ssm_delta_fwd(t["q"], t["k"], t["v"], t["delta"], t["A"], t["beta"], delta_bias=t["delta_bias"],
+                               initial_state=state, final_state=state)
+    torch.cuda.synchronize()
+    assert s2 is state and torch.equal(y1, y2) and torch.equal(s1, s2)
+
+
+def test_without_final_state():
+    x = I.random_delta_inputs(np.random.default_rng(1520), 1, 100, 1, 2, 64, 64)
+    say("delta without a final state")
+    y1, _ = run(x, "bf16")
+    y2, s2 = run(x, "bf16", return_final_state=False)
+    assert s2 is None and torch.equal(y1, y2)
