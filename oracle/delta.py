@@ -46,6 +46,27 @@ def delta_fwd(q, k, v, delta, A, beta, delta_bias=None, softplus=True, sigmoid=T
     return y, S
 
 
+def delta_magnitudes(q, k, v, delta, A, beta, delta_bias=None, softplus=True, sigmoid=True, scale=None,
+                     initial_state=None, cu_seqlens=None):
+    """The sums of magnitudes behind y and the final states: scale |S|_t |q_t| and |S|_L with |S|_t = a_t |S|_{t-1} +
+    |u_t| |k_t|^T (their layouts): what roundings of single operands of their products can move them by, in units of
+    the roundings' relative size."""
+    x = dict(q=q, k=k, v=v, delta=delta, A=A, beta=beta, bias=delta_bias)
+    _, _, (kept, rows, a, b, step, raw, kh, qh, sc) = _walk(**x, softplus=softplus, sigmoid=sigmoid, scale=scale,
+                                                            h0=initial_state, cu=cu_seqlens, keep=True)
+    v = _f64(v)
+    out, last = np.zeros_like(v), []
+    for i, (r, lo, hi) in enumerate(rows):
+        M = np.abs(kept[i][0])
+        for t in range(lo, hi):
+            old = a[r, t, :, None, None] * kept[i][t - lo]
+            u = b[r, t, :, None] * (v[r, t] - np.einsum("hpn,hn->hp", old, kh[r, t]))
+            M = np.abs(a[r, t, :, None, None]) * M + np.abs(u)[..., None] * np.abs(kh[r, t])[:, None, :]
+            out[r, t] = abs(sc) * np.einsum("hpn,hn->hp", M, np.abs(qh[r, t]))
+        last.append(M)
+    return out, np.stack(last)
+
+
 def _walk(q, k, v, delta, A, beta, bias, softplus, sigmoid, scale, h0, cu, y_before=None, keep=False):
     q, k, v, delta, A, beta, bias, h0 = map(_f64, (q, k, v, delta, A, beta, bias, h0))
     batch, L, H, P = v.shape

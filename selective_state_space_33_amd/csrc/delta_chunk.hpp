@@ -1,0 +1,160 @@
+// delta_chunk.hpp -- what the chunked kernels of the gated delta rule share:
+// the chunk's mathematics, its image in the workspace, fp16 pairs and the
+// layout of MFMA operands.
+//
+// A chunk of C = 64 tokens that starts from the state S0 (here dstate x
+// headdim), with cs_t the sum of step A up to t (inclusive, chunk-local):
+//   N_tj = e^{cs_t - cs_j} k_t . k_j            (j < t)
+//   T    = (I + diag(b) N)^-1                    (unit lower triangular)
+//   X    = diag(b) (V - diag(e^cs) K S0),   U = T X
+//   Y    = scale (diag(e^cs) Q S0 + P U),   P_tj = e^{cs_t - cs_j} q_t . k_j  (j <= t)
+//   S_C  = e^{cs_C} S0 + K^T diag(e^{cs_C - cs}) U
+// T, P and the fades depend on q, k and the gates alone, not on the state, so
+// a first kernel (delta_prep_kernel) forms them for all chunks at once; the
+// second (delta_walk_kernel) walks each sequence's chunks in order.  The
+// columns of S0, X, U and Y (value channels) never meet, so the walk cuts a
+// head into tiles of 16 channels.
+//
+// Operand order.  An accumulator of v_mfma_f32_16x16x32_f16 holds rows 4 lq + i
+// (i < 4) of column lr in lane 16 lq + lr.  The same registers, two row tiles
+// side by side, are a B (or, transposed, an A) operand whose K index runs
+// 4 lq + {0..3}, 16 + 4 lq + {0..3} in a lane: a product does not care in which
+// order K runs as long as both operands agree.  So the state, X and U go from
+// one product into the next in registers, and the other operands (K, Q, T, P)
+// are stored or read in that order ("paired order").
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace ssm {
+
+constexpr int kDeltaC = 64;  // tokens per chunk
+
+// The chunk image, one per (chunk slot, head): operand fragments in paired
+// order, 64 lanes x 16 bytes each.  T and P are lower triangular, so of a
+// 64 x 64 matrix only six fragments (row tile t, column pair m <= t / 2) hold
+// anything: index kFragOf(t, m).
+constexpr int kFrag = 1024;                  // bytes of a fragment
+constexpr int kImgThi = 0;                   // T, fp16 hi
+constexpr int kImgTlo = 6 * kFrag;           // T, fp16 lo
+constexpr int kImgP = 12 * kFrag;            // P, fp16
+constexpr int kImgGrow = 18 * kFrag;         // e^{cs_t}
+constexpr int kImgLeft = kImgGrow + 256;     // e^{cs_C - cs_t}
+constexpr int kImgBeta = kImgGrow + 512;     // b_t (0 behind the sequence's end)
+constexpr int kImgBytes = kImgGrow + 1024;
+__host__ __device__ constexpr int frag_of(int t, int m) { return t < 2 ? t : 2 + 2 * (t - 2) + m; }
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4_t mfma_f16(f16x8_t a, f16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Two accumulator tiles as one operand: rounded to fp16 (nearest even), and as
+// a pair hi + lo (hi = fp16(v), lo = fp16(v - hi): 22 significant bits).
+__device__ __forceinline__ f16x8_t pair_f16(f32x4_t a, f32x4_t b) {
+  const f16x4_t x = __builtin_convertvector(a, f16x4_t), y = __builtin_convertvector(b, f16x4_t);
+  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ f32x4_t f16_rest(f32x4_t v, f16x4_t h) {
+  f32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __builtin_fmaf(-1.0f, static_cast<float>(h[i]), v[i]);
+  return r;
+}
+__device__ __forceinline__ void split_f16(f32x4_t a, f32x4_t b, f16x8_t& hi, f16x8_t& lo) {
+  const f16x4_t x = __builtin_convertvector(a, f16x4_t), y = __builtin_convertvector(b, f16x4_t);
+  hi = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  lo = pair_f16(f16_rest(a, x), f16_rest(b, y));
+}
+
+// Eight bf16 values as fp16 (exact from 2^-17 to 65504 in magnitude).
+__device__ __forceinline__ u32x4_t bf16x8_as_f16(u32x4_t v) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f16x2_t h = __builtin_convertvector((f32x2_t){bf16_lo(v[i]), bf16_hi(v[i])}, f16x2_t);
+    r[i] = __builtin_bit_cast(uint32_t, h);
+  }
+  return r;
+}
+
+// Where run j (four elements) of a 32-element block sits in paired order.
+__device__ __forceinline__ constexpr int paired_run(int j) { return j < 4 ? 2 * j : 2 * j - 7; }
+
+// An operand fragment whose K index is the row of a row-major fp16 array in
+// LDS (rows k0 .. k0 + 31 in paired order, this lane's column col0 + lr): two
+// transposed reads (ds_read_b64_tr_b16), each handing lane i of 16 the column
+// i of four rows that its lanes address as 4 x 4 runs.
+__device__ __forceinline__ u32x2_t lds_tr4(const uint16_t* base, int row0, int col0, int stride, int lr) {
+  typedef short v4i16 __attribute__((ext_vector_type(4)));
+  const uint16_t* a = base + (row0 + (lr >> 2)) * stride + col0 + 4 * (lr & 3);
+  const v4i16 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(a));
+  return __builtin_bit_cast(u32x2_t, v);
+}
+__device__ __forceinline__ f16x8_t lds_col_frag(const uint16_t* base, int k0, int col0, int stride, int lr, int lq) {
+  const u32x2_t a = lds_tr4(base, k0 + 4 * lq, col0, stride, lr);
+  const u32x2_t b = lds_tr4(base, k0 + 16 + 4 * lq, col0, stride, lr);
+  return __builtin_bit_cast(f16x8_t, u32x4_t{a[0], a[1], b[0], b[1]});
+}
+
+// Sequence s of the call: its first token in the flat [batch * L] token axis,
+// its length, and its first chunk slot.  Packed offsets are clamped into
+// [0, L]; slot cu[s] / 64 + s leaves every sequence room for its chunks, since
+// ceil(len / 64) <= floor(end / 64) - floor(start / 64) + 1.
+struct DeltaSeq {
+  int64_t tok, len, slot;
+};
+__device__ __forceinline__ DeltaSeq delta_seq(const int64_t* cu, int64_t s, int64_t L, int64_t chunks_per_row) {
+  DeltaSeq d;
+  if (!cu) {
+    d.tok = s * L;
+    d.len = L;
+    d.slot = s * chunks_per_row;
+    return d;
+  }
+  const int64_t a = cu[s], b = cu[s + 1];
+  d.tok = a < 0 ? 0 : (a > L ? L : a);
+  const int64_t e = b < d.tok ? d.tok : (b > L ? L : b);
+  d.len = e - d.tok;
+  d.slot = d.tok / kDeltaC + s;
+  return d;
+}
+
+// Workgroups are dealt round-robin to the eight XCDs; giving each XCD a run of
+// consecutive units lets neighbours that read the same rows share its L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
+  const int64_t q = n / 8, r = n % 8, x = i % 8;
+  return x * q + (x < r ? x : r) + i / 8;
+}
+
+struct DeltaChunkParams {
+  const void* q;       // [tokens][G][N] bf16
+  const void* k;
+  const void* v;       // [tokens][H][P] bf16
+  const void* delta;   // [tokens][H] bf16 (raw)
+  const float* A;      // [H]
+  const void* beta;    // [tokens][H] bf16
+  const float* bias;   // [H] (nullable)
+  const float* h0;     // [rows][H][P][N] (nullable); may be hT
+  float* hT;           // (nullable)
+  const int64_t* cu;   // (nullable)
+  void* y;
+  char* img;           // [slots][H][kImgBytes]
+  unsigned* words;     // workspace header
+  int64_t rows;        // sequences
+  int64_t L, H, G, P;
+  int64_t chunks;      // chunks per batch row (no cu)
+  int64_t slots;       // chunk slots in all
+  int softplus, sigmoid;
+  float scale;
+};
+
+}  // namespace ssm

@@ -1,0 +1,220 @@
+// delta_prep_kernel.hpp -- the part of the chunked gated delta rule that does
+// not depend on the state: per chunk and head T = (I + diag(b) N)^-1, P and
+// the fades (delta_chunk.hpp), all chunks in parallel.
+//
+// One workgroup of four wavefronts per (chunk, head).  K and Q of the chunk
+// sit in LDS as they come (bf16, so the products K K^T and K Q^T are exact up
+// to their fp32 sums).  cs is summed in fp64 and kept as a pair of floats:
+// differences of neighbours deep in a fast-fading chunk would otherwise lose
+// bits.  The inverse is a forward substitution: the four 16 x 16 diagonal
+// blocks at once in one wavefront (a lane a column), then block column j in
+// wavefront j, T_ij = -T_ii sum_l M_il T_lj, on fp32 MFMA (16x16x4), whose
+// accumulators again serve as the next product's operand.
+#pragma once
+
+#include "delta_chunk.hpp"
+#include "delta_step_kernel.hpp"
+
+namespace ssm {
+
+constexpr int kPrepLd = 68;  // floats per row of the 64 x 64 fp32 arrays (16-byte aligned, banks staggered)
+
+// acc + A B over 16: A rows from LDS (row-major fp32, this lane's row at a), B an accumulator tile.
+__device__ __forceinline__ f32x4_t mfma_f32_tile(const float* a, f32x4_t b, f32x4_t acc) {
+  const f32x4_t av = *reinterpret_cast<const f32x4_t*>(a);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(av[r], b[r], acc, 0, 0, 0);
+  return acc;
+}
+
+// Block column J of T from the diagonal blocks in sT, written to sT.
+template <int J> __device__ __forceinline__ void prep_column(const float* sM, float* sT, int lr, int lq) {
+  f32x4_t t[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) t[J][r] = sT[(16 * J + 4 * lq + r) * kPrepLd + 16 * J + lr];
+#pragma unroll
+  for (int i = J + 1; i < 4; ++i) {
+    f32x4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int l = J; l < i; ++l) z = mfma_f32_tile(&sM[(16 * i + lr) * kPrepLd + 16 * l + 4 * lq], t[l], z);
+    t[i] = mfma_f32_tile(&sT[(16 * i + lr) * kPrepLd + 16 * i + 4 * lq], z, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      t[i][r] = -t[i][r];
+      sT[(16 * i + 4 * lq + r) * kPrepLd + 16 * J + lr] = t[i][r];
+    }
+  }
+}
+
+template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkParams p) {
+  constexpr int SB = DK + 8;  // bf16 row stride
+  __shared__ __attribute__((aligned(16))) uint16_t sK[kDeltaC * SB], sQ[kDeltaC * SB];
+  __shared__ __attribute__((aligned(16))) float sM[kDeltaC * kPrepLd], sT[kDeltaC * kPrepLd];
+  __shared__ __attribute__((aligned(16))) float sChi[kDeltaC], sClo[kDeltaC], sBeta[kDeltaC];
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int lr = lane & 15, lq = lane >> 4;
+  if (p.words && blockIdx.x == 0 && tid < 4) p.words[tid] = 0u;
+  const int64_t id = xcd_order(blockIdx.x, static_cast<int64_t>(p.slots) * p.H);
+  const int64_t slot = id / p.H, h = id % p.H, g = h / (p.H / p.G);
+  // the sequence of this slot: the last one that starts at or before it
+  int64_t s = 0;
+  if (p.cu) {
+    int64_t hi = p.rows - 1;
+    while (s < hi) {
+      const int64_t mid = (s + hi + 1) / 2;
+      if (delta_seq(p.cu, mid, p.L, 0).slot <= slot)
+        s = mid;
+      else
+        hi = mid - 1;
+    }
+  } else {
+    s = slot / p.chunks;
+  }
+  const DeltaSeq sq = delta_seq(p.cu, s, p.L, p.chunks);
+  const int64_t c0 = (slot - sq.slot) * kDeltaC;
+  if (slot < sq.slot || c0 >= sq.len) return;  // a slot of no chunk (the same for the whole workgroup)
+  const int nt = static_cast<int>(sq.len - c0 < kDeltaC ? sq.len - c0 : kDeltaC);
+  const int64_t tok = sq.tok + c0;
+
+  // ---- K, Q (rows behind the end are zero) and the gates
+  {
+    const int64_t rowe = p.G * DK;
+    const int64_t base = tok * rowe + g * DK, bytes = ((nt - 1) * rowe + DK) * 2;
+    const rsrc_t rk = make_rsrc(static_cast<const uint16_t*>(p.k) + base, bytes);
+    const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(p.q) + base, bytes);
+    constexpr int PER = kDeltaC * DK / 8 / 256;
+    u32x4_t kv[PER], qv[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + 256 * i, row = e / (DK / 8), col = (e % (DK / 8)) * 8;
+      const int off = static_cast<int>((row * rowe + col) * 2);
+      kv[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0));
+      qv[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
+    }
+    if (w == 0) {
+      const bool live = lane < nt;
+      float step = 0.0f, b = 0.0f;
+      if (live) {
+        const float raw = load_elem<BF16>(p.delta, (tok + lane) * p.H + h) + (p.bias ? p.bias[h] : 0.0f);
+        step = p.softplus ? softplus_f(raw) : raw;
+        const float braw = load_elem<BF16>(p.beta, (tok + lane) * p.H + h);
+        b = p.sigmoid ? sigmoid_f(braw) : braw;
+      }
+      double cs = static_cast<double>(step) * static_cast<double>(p.A[h]);
+      cs = live ? cs : 0.0;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const double up = __shfl_up(cs, o, 64);
+        cs += lane >= o ? up : 0.0;
+      }
+      const double end = __shfl(cs, 63, 64);
+      const float chi = static_cast<float>(cs);
+      sChi[lane] = chi;
+      sClo[lane] = static_cast<float>(cs - static_cast<double>(chi));
+      sBeta[lane] = b;
+      float* img = reinterpret_cast<float*>(p.img + id * kImgBytes + kImgGrow);
+      img[lane] = __builtin_amdgcn_exp2f(chi * kLog2e);
+      img[64 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(end - cs) * kLog2e);
+      img[128 + lane] = b;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + 256 * i, row = e / (DK / 8), col = (e % (DK / 8)) * 8;
+      *reinterpret_cast<u32x4_t*>(&sK[row * SB + col]) = kv[i];
+      *reinterpret_cast<u32x4_t*>(&sQ[row * SB + col]) = qv[i];
+    }
+  }
+  __syncthreads();
+
+  auto frag = [&](const uint16_t* a, int tile, int kk) {
+    return *reinterpret_cast<const bf16x8_t*>(&a[(16 * tile + lr) * SB + 32 * kk + 8 * lq]);
+  };
+  // e^{cs_t - cs_j}
+  auto fade = [&](int t, int j) {
+    return __builtin_amdgcn_exp2f(((sChi[t] - sChi[j]) + (sClo[t] - sClo[j])) * kLog2e);
+  };
+  // ---- M = diag(b) N: row tile w, column tiles 0 .. w
+  for (int jt = 0; jt <= w; ++jt) {
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kk = 0; kk < DK / 32; ++kk)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, w, kk), frag(sK, jt, kk), acc, 0, 0, 0);
+    const int j = 16 * jt + lr;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * w + 4 * lq + r;
+      sM[t * kPrepLd + j] = j < t ? sBeta[t] * fade(t, j) * acc[r] : 0.0f;
+    }
+  }
+  __syncthreads();
+  if (w == 0) {
+    // ---- the diagonal blocks' inverses: lane (block, column c) solves (I + M_bb) x = e_c
+    const int b0 = 16 * lq, c = lr;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float acc0 = i == c ? 1.0f : 0.0f, acc1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) {
+        const float m = sM[(b0 + i) * kPrepLd + b0 + j];
+        if (j & 1)
+          acc1 = __builtin_fmaf(-m, x[j], acc1);
+        else
+          acc0 = __builtin_fmaf(-m, x[j], acc0);
+      }
+      x[i] = acc0 + acc1;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sT[(b0 + i) * kPrepLd + b0 + c] = x[i];
+  } else {
+    // ---- P meanwhile: the tiles of K Q^T leave four consecutive j of token t = lr in a lane, half a fragment
+    const int first = w == 1 ? 3 : (w == 2 ? 2 : 0), last = w == 3 ? 1 : first;
+    for (int tt = first; tt <= last; ++tt) {
+      for (int m = 0; m <= tt / 2; ++m) {
+        f32x4_t half[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int jt = 2 * m + u, t = 16 * tt + lr;
+          f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (jt <= tt) {
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk)
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, jt, kk), frag(sQ, tt, kk), acc, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int j = 16 * jt + 4 * lq + r;
+              acc[r] = j <= t ? fade(t, j) * acc[r] : 0.0f;
+            }
+          }
+          half[u] = acc;
+        }
+        // fp16: P meets u (fp16 too) in y alone, which is stored with 8 significant bits
+        *reinterpret_cast<f16x8_t*>(p.img + id * kImgBytes + kImgP + frag_of(tt, m) * kFrag + lane * 16) =
+            pair_f16(half[0], half[1]);
+      }
+    }
+  }
+  __syncthreads();
+  if (w == 0)
+    prep_column<0>(sM, sT, lr, lq);
+  else if (w == 1)
+    prep_column<1>(sM, sT, lr, lq);
+  else if (w == 2)
+    prep_column<2>(sM, sT, lr, lq);
+  __syncthreads();
+  // ---- T as fragments, hi + lo
+  for (int e = tid; e < 6 * 64; e += 256) {
+    const int f = e >> 6, ln = e & 63, row = ln & 15, q4 = 4 * (ln >> 4);
+    const int t = f < 2 ? f : 2 + ((f - 2) >> 1), m = f < 2 ? 0 : (f & 1);
+    const float* a = &sT[(16 * t + row) * kPrepLd + 32 * m + q4];
+    const f32x4_t x0 = *reinterpret_cast<const f32x4_t*>(a);
+    const f32x4_t x1 = 2 * m + 1 <= t ? *reinterpret_cast<const f32x4_t*>(a + 16) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    f16x8_t hi, lo;
+    split_f16(x0, x1, hi, lo);
+    char* out = p.img + id * kImgBytes + f * kFrag + ln * 16;
+    *reinterpret_cast<f16x8_t*>(out + kImgThi) = hi;
+    *reinterpret_cast<f16x8_t*>(out + kImgTlo) = lo;
+  }
+}
+
+}  // namespace ssm

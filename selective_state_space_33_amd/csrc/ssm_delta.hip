@@ -2,9 +2,12 @@
 // one-token step (declared with their contracts in include/ssm_scan.h).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "delta_host.hpp"
+#include "delta_prep_kernel.hpp"
 #include "delta_step_kernel.hpp"
+#include "delta_walk_kernel.hpp"
 #include "host_common.hpp"
 #include "ssm_scan.h"
 
@@ -64,6 +67,37 @@ DeltaStepParams step_params(const DeltaArgs& a) {
   return p;
 }
 
+// ---- the chunked plan
+bool delta_chunked(int64_t L, int64_t heads, int64_t headdim, int64_t dstate, int64_t nseq, ssm_dtype_t dt) {
+  if (dt != SSM_DTYPE_BF16 || dstate > 128 || headdim % 16 != 0) return false;
+  // a chunk's rows are addressed with 32-bit byte offsets
+  if (heads * headdim > (1 << 23) || heads * dstate > (1 << 23)) return false;
+  const char* e = getenv("SSM_DELTA_CHUNKED");
+  if (e) return atoi(e) != 0;
+  return L / (nseq > 0 ? nseq : 1) > 16;
+}
+int64_t delta_slots(int64_t batch, int64_t L, int64_t nseq) {
+  return nseq > 0 ? L / kDeltaC + nseq : batch * ((L + kDeltaC - 1) / kDeltaC);
+}
+constexpr size_t kDeltaHeader = 256;
+
+template <int DK> hipError_t run_chunked(DeltaChunkParams& p, hipStream_t s) {
+  const int64_t grid = p.slots * p.H;
+  if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t tiles = p.P / 16;
+  if (tiles > 4) {
+    const int64_t wgs = p.rows * p.H * ((tiles + 7) / 8);
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 2>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, s, p);
+  } else {
+    const int64_t wgs = p.rows * p.H * ((tiles + 3) / 4);
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 1>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 }  // namespace ssm
 
@@ -90,8 +124,12 @@ extern "C" ssm_status_t ssm_delta_update(float* state, const void* q, const void
 
 extern "C" size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int64_t headdim,
                                                int64_t ngroups, int64_t dstate, int64_t nseq, ssm_dtype_t dt) {
-  (void)batch, (void)L, (void)heads, (void)headdim, (void)ngroups, (void)dstate, (void)nseq, (void)dt;
-  return 0;
+  if (!delta_sizes_ok(batch, L, heads, headdim, ngroups, dstate) || (dt != SSM_DTYPE_F32 && dt != SSM_DTYPE_BF16))
+    return 0;
+  if ((nseq > 0 && batch != 1) || nseq < 0) return 0;
+  if (!delta_shape_supported(nseq > 0 ? nseq : batch, L, heads, headdim, dstate)) return 0;
+  if (!delta_chunked(L, heads, headdim, dstate, nseq, dt)) return 0;
+  return kDeltaHeader + static_cast<size_t>(delta_slots(batch, L, nseq)) * heads * kImgBytes;
 }
 
 extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
@@ -106,12 +144,47 @@ extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* 
                        scale, dt};
   const ssm_status_t st = check_delta_args(a, y, final_state);
   if (st != SSM_OK) return st;
-  (void)workspace, (void)workspace_bytes;
-  DeltaStepParams p = step_params(a);
+  if (!delta_chunked(L, heads, headdim, dstate, nseq, dt) || !delta_aligned(y, 8)) {
+    DeltaStepParams p = step_params(a);
+    p.hT = final_state;
+    p.y = y;
+    const int64_t units = (cu_seqlens ? nseq : batch) * heads;
+    const hipError_t e = dt == SSM_DTYPE_F32 ? run_step<F32>(p, units, dstate, stream)
+                                             : run_step<BF16>(p, units, dstate, stream);
+    return e == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+  }
+  const size_t need = ssm_delta_fwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq, dt);
+  if (!workspace || workspace_bytes < need || !delta_aligned(workspace, 256)) return SSM_ERR_INVALID_ARG;
+  DeltaChunkParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.delta = delta;
+  p.A = A;
+  p.beta = beta;
+  p.bias = delta_bias;
+  p.h0 = initial_state;
   p.hT = final_state;
+  p.cu = cu_seqlens;
   p.y = y;
-  const int64_t units = (cu_seqlens ? nseq : batch) * heads;
-  const hipError_t e = dt == SSM_DTYPE_F32 ? run_step<F32>(p, units, dstate, stream)
-                                           : run_step<BF16>(p, units, dstate, stream);
+  p.words = static_cast<unsigned*>(workspace);
+  p.img = static_cast<char*>(workspace) + kDeltaHeader;
+  p.rows = cu_seqlens ? nseq : batch;
+  p.L = L;
+  p.H = heads;
+  p.G = ngroups;
+  p.P = headdim;
+  p.chunks = (L + kDeltaC - 1) / kDeltaC;
+  p.slots = delta_slots(batch, L, cu_seqlens ? nseq : 0);
+  p.softplus = a.softplus;
+  p.sigmoid = a.sigmoid;
+  p.scale = scale;
+  hipError_t e = hipErrorInvalidValue;
+  switch (dstate) {
+    case 32: e = run_chunked<32>(p, stream); break;
+    case 64: e = run_chunked<64>(p, stream); break;
+    case 96: e = run_chunked<96>(p, stream); break;
+    case 128: e = run_chunked<128>(p, stream); break;
+  }
   return e == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
