@@ -5,14 +5,16 @@
 // A chunk of C = 64 tokens that starts from the state S0 (here dstate x
 // headdim), with cs_t the sum of step A up to t (inclusive, chunk-local):
 //   N_tj = e^{cs_t - cs_j} k_t . k_j            (j < t)
-//   T    = (I + diag(b) N)^-1                    (unit lower triangular)
-//   X    = diag(b) (V - diag(e^cs) K S0),   U = T X
-//   Y    = scale (diag(e^cs) Q S0 + P U),   P_tj = e^{cs_t - cs_j} q_t . k_j  (j <= t)
-//   S_C  = e^{cs_C} S0 + K^T diag(e^{cs_C - cs}) U
+//   T    = (I + N diag(b))^-1                    (unit lower triangular)
+//   X    = V - diag(e^cs) K S0,   R = T X,   U = diag(b) R
+//   Y    = diag(scale e^cs) Q S0 + P R,  P_tj = scale e^{cs_t - cs_j} (q_t . k_j) b_j  (j <= t)
+//   S_C  = e^{cs_C} S0 + K^T diag(e^{cs_C - cs} b) R
+// R is what each token adds, v_t minus what the state answers its key; b only
+// meets it in P and in the last line, so a b of zero divides nothing.
 // T, P and the fades depend on q, k and the gates alone, not on the state, so
 // a first kernel (delta_prep_kernel) forms them for all chunks at once; the
 // second (delta_walk_kernel) walks each sequence's chunks in order.  The
-// columns of S0, X, U and Y (value channels) never meet, so the walk cuts a
+// columns of S0, X, R and Y (value channels) never meet, so the walk cuts a
 // head into tiles of 16 channels.
 //
 // Operand order.  An accumulator of v_mfma_f32_16x16x32_f16 holds rows 4 lq + i
@@ -26,6 +28,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <utility>
 
 #include "common.hpp"
 
@@ -42,9 +46,9 @@ constexpr int kImgThi = 0;                   // T, fp16 hi
 constexpr int kImgTlo = 6 * kFrag;           // T, fp16 lo
 constexpr int kImgP = 12 * kFrag;            // P, fp16
 constexpr int kImgGrow = 18 * kFrag;         // e^{cs_t}
-constexpr int kImgLeft = kImgGrow + 256;     // e^{cs_C - cs_t}
-constexpr int kImgBeta = kImgGrow + 512;     // b_t (0 behind the sequence's end)
-constexpr int kImgBytes = kImgGrow + 1024;
+constexpr int kImgOut = kImgGrow + 256;      // scale e^{cs_t}
+constexpr int kImgLeft = kImgGrow + 512;     // e^{cs_C - cs_t} b_t (0 behind the sequence's end)
+constexpr int kImgBytes = kImgGrow + 768;
 __host__ __device__ constexpr int frag_of(int t, int m) { return t < 2 ? t : 2 + 2 * (t - 2) + m; }
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -63,10 +67,15 @@ __device__ __forceinline__ f16x8_t pair_f16(f32x4_t a, f32x4_t b) {
   const f16x4_t x = __builtin_convertvector(a, f16x4_t), y = __builtin_convertvector(b, f16x4_t);
   return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
+// v - h exactly, h an fp16 value: one mixed-precision FMA each (the compiler turns half of them into a conversion and
+// a subtraction when it may choose).
 __device__ __forceinline__ f32x4_t f16_rest(f32x4_t v, f16x4_t h) {
+  const u32x2_t w = __builtin_bit_cast(u32x2_t, h);
   f32x4_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = __builtin_fmaf(-1.0f, static_cast<float>(h[i]), v[i]);
+  asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r[0]) : "v"(w[0]), "v"(v[0]));
+  asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r[1]) : "v"(w[0]), "v"(v[1]));
+  asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r[2]) : "v"(w[1]), "v"(v[2]));
+  asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r[3]) : "v"(w[1]), "v"(v[3]));
   return r;
 }
 __device__ __forceinline__ void split_f16(f32x4_t a, f32x4_t b, f16x8_t& hi, f16x8_t& lo) {
@@ -86,23 +95,40 @@ __device__ __forceinline__ u32x4_t bf16x8_as_f16(u32x4_t v) {
   return r;
 }
 
-// Where run j (four elements) of a 32-element block sits in paired order.
-__device__ __forceinline__ constexpr int paired_run(int j) { return j < 4 ? 2 * j : 2 * j - 7; }
-
-// An operand fragment whose K index is the row of a row-major fp16 array in
-// LDS (rows k0 .. k0 + 31 in paired order, this lane's column col0 + lr): two
-// transposed reads (ds_read_b64_tr_b16), each handing lane i of 16 the column
-// i of four rows that its lanes address as 4 x 4 runs.
-__device__ __forceinline__ u32x2_t lds_tr4(const uint16_t* base, int row0, int col0, int stride, int lr) {
+// K and Q of a chunk in LDS: fp16 rows of DK elements, 4 x odd dwords apart.
+// Sixteen rows x two neighbouring 8-byte runs (a fragment of rows: two runs 32
+// bytes apart a lane, one read of 2 x 8 bytes) then touch every bank once, and
+// the transposed reads of a fragment of columns (eight rows x 32 bytes) every
+// bank twice.  (An 8 x odd stride turns that round; a swizzle that serves both
+// needs an address register per fragment, which the walk does not have.)
+template <int DK> constexpr int kRowLd = DK + 8;
+// 32 K indices from 32 kk of row r in paired order (this lane: runs lq and lq + 4).
+template <int DK> __device__ __forceinline__ f16x8_t lds_row_frag(const uint16_t* base, int r, int kk, int lq) {
+  const uint16_t* a = base + r * kRowLd<DK> + 32 * kk + 4 * lq;
+  const u32x2_t x = *reinterpret_cast<const u32x2_t*>(a), y = *reinterpret_cast<const u32x2_t*>(a + 16);
+  return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
+}
+// Transposed LDS read (ds_read_b64_tr_b16): lane i of 16 receives, of the four
+// rows that the 16 lanes address as 4 x 4 runs (lane i: row i / 4, run i % 4),
+// column i.
+__device__ __forceinline__ u32x2_t lds_tr4(const uint16_t* a) {
   typedef short v4i16 __attribute__((ext_vector_type(4)));
-  const uint16_t* a = base + (row0 + (lr >> 2)) * stride + col0 + 4 * (lr & 3);
   const v4i16 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)(a));
   return __builtin_bit_cast(u32x2_t, v);
 }
-__device__ __forceinline__ f16x8_t lds_col_frag(const uint16_t* base, int k0, int col0, int stride, int lr, int lq) {
-  const u32x2_t a = lds_tr4(base, k0 + 4 * lq, col0, stride, lr);
-  const u32x2_t b = lds_tr4(base, k0 + 16 + 4 * lq, col0, stride, lr);
-  return __builtin_bit_cast(f16x8_t, u32x4_t{a[0], a[1], b[0], b[1]});
+// A fragment whose K index is the row of such an array: rows k0 .. k0 + 31 in paired order, columns 16 d + lr.
+template <int DK> __device__ __forceinline__ f16x8_t lds_col_frag(const uint16_t* base, int k0, int d, int lr, int lq) {
+  const uint16_t* a = base + (k0 + 4 * lq + (lr >> 2)) * kRowLd<DK> + 16 * d + 4 * (lr & 3);
+  const u32x2_t x = lds_tr4(a), y = lds_tr4(a + 16 * kRowLd<DK>);
+  return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
+}
+
+// f(IC<0>) .. f(IC<N - 1>): a loop whose index is a constant in the body.
+template <class F, int... I> __device__ __forceinline__ void static_for_each(F&& f, std::integer_sequence<int, I...>) {
+  (f(IC<I>{}), ...);
+}
+template <int N, class F> __device__ __forceinline__ void static_for(F&& f) {
+  static_for_each(f, std::make_integer_sequence<int, N>{});
 }
 
 // Sequence s of the call: its first token in the flat [batch * L] token axis,

@@ -1,5 +1,5 @@
 // delta_prep_kernel.hpp -- the part of the chunked gated delta rule that does
-// not depend on the state: per chunk and head T = (I + diag(b) N)^-1, P and
+// not depend on the state: per chunk and head T = (I + N diag(b))^-1, P and
 // the fades (delta_chunk.hpp), all chunks in parallel.
 //
 // One workgroup of four wavefronts per (chunk, head).  K and Q of the chunk
@@ -113,9 +113,10 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
       sClo[lane] = static_cast<float>(cs - static_cast<double>(chi));
       sBeta[lane] = b;
       float* img = reinterpret_cast<float*>(p.img + id * kImgBytes + kImgGrow);
-      img[lane] = __builtin_amdgcn_exp2f(chi * kLog2e);
-      img[64 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(end - cs) * kLog2e);
-      img[128 + lane] = b;
+      const float grow = __builtin_amdgcn_exp2f(chi * kLog2e);
+      img[lane] = grow;
+      img[64 + lane] = p.scale * grow;
+      img[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(end - cs) * kLog2e) * b;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -133,7 +134,7 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
   auto fade = [&](int t, int j) {
     return __builtin_amdgcn_exp2f(((sChi[t] - sChi[j]) + (sClo[t] - sClo[j])) * kLog2e);
   };
-  // ---- M = diag(b) N: row tile w, column tiles 0 .. w
+  // ---- M = N diag(b): row tile w, column tiles 0 .. w
   for (int jt = 0; jt <= w; ++jt) {
     f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -143,7 +144,7 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * w + 4 * lq + r;
-      sM[t * kPrepLd + j] = j < t ? sBeta[t] * fade(t, j) * acc[r] : 0.0f;
+      sM[t * kPrepLd + j] = j < t ? sBeta[j] * fade(t, j) * acc[r] : 0.0f;
     }
   }
   __syncthreads();
@@ -183,12 +184,12 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int j = 16 * jt + 4 * lq + r;
-              acc[r] = j <= t ? fade(t, j) * acc[r] : 0.0f;
+              acc[r] = j <= t ? p.scale * sBeta[j] * fade(t, j) * acc[r] : 0.0f;
             }
           }
           half[u] = acc;
         }
-        // fp16: P meets u (fp16 too) in y alone, which is stored with 8 significant bits
+        // fp16: P meets R (fp16 too) in y alone, which is stored with 8 significant bits
         *reinterpret_cast<f16x8_t*>(p.img + id * kImgBytes + kImgP + frag_of(tt, m) * kFrag + lane * 16) =
             pair_f16(half[0], half[1]);
       }

@@ -1,13 +1,19 @@
 // delta_walk_kernel.hpp -- the chunked gated delta rule's walk over a
 // sequence (delta_chunk.hpp has the mathematics and the operand order).
 //
-// A wavefront owns NC tiles of 16 value channels with their whole state
-// (dstate x 16 NC, fp32 accumulators) and takes a chunk from S0 to S_C without
-// exchanging anything with its neighbours; the W wavefronts of a workgroup
-// share the chunk's K, Q, T, P and fades in LDS, double-buffered, so a chunk
-// costs one barrier.  Per chunk and tile (dstate 128) 104 MFMAs 16x16x32:
-// K S0 32 (S0 as fp16 hi + lo), T X 18 (both as pairs, without lo x lo),
-// K^T U 32, Q S0 16 and P U 6 (one product each: y is stored with 8 bits).
+// A wavefront owns a tile of 16 value channels with its whole state (dstate x
+// 16, fp32 accumulators) and takes a chunk from S0 to S_C without exchanging
+// anything with its neighbours; the W wavefronts of a workgroup share the
+// chunk's K, Q, T, P and fades in LDS, double-buffered, so a chunk costs one
+// barrier.  Per chunk (dstate 128) 104 MFMAs 16x16x32: K S0 32 (S0 as fp16
+// hi + lo), T X 18 (both as pairs, without lo x lo), K^T R 32, Q S0 16 and
+// P R 6 (one product each: y is stored with 8 bits).
+//
+// The chain K S0 -> X -> T X -> R -> K^T R is serial, and only two wavefronts
+// share a SIMD, so the order of the instructions matters: fragments are read
+// from LDS one step ahead of the products that take them, and scheduling
+// fences keep the compiler from moving the reads next to their use (where each
+// one's latency would show).
 //
 // Precision.  K and Q convert to fp16 exactly.  Everything on the way from
 // state to state is a pair of fp16 (22 bits) with fp32 accumulation.
@@ -17,23 +23,41 @@
 
 namespace ssm {
 
-template <int DK, int W, int NC> struct DeltaWalkLds {
-  // K twice: by rows for K S0 (paired order, 16-byte fragment reads: a row
-  // stride of 4 x odd dwords), and plain for the transposed reads of K^T U
-  // (8 x odd dwords: eight rows of a read touch all banks once).
-  static constexpr int SP = DK + 8, ST = DK + 16;
-  __attribute__((aligned(16))) uint16_t k[kDeltaC * SP];
-  __attribute__((aligned(16))) uint16_t kt[kDeltaC * ST];
-  __attribute__((aligned(16))) uint16_t q[kDeltaC * SP];
+// A channel tile that the head does not have is addressed here: behind every resource (they are cut to this length,
+// and a chunk's offsets, 64 rows of at most 2^23 bytes, stay below half of it), so loads return zero and stores are
+// dropped.
+constexpr int kPastEnd = 0x40000000;
+
+// A tensor's next chunk: where it starts, and the length of the resource over it.  Only the last chunk's has to end
+// where the sequence does; past it there is nothing.
+struct DeltaStream {
+  char* base;
+  int64_t step;
+  int tail;
+  __device__ __forceinline__ DeltaStream(const void* p, int64_t chunk, int64_t last)
+      : base(static_cast<char*>(const_cast<void*>(p))), step(chunk), tail(static_cast<int>(last)) {}
+  // left: chunks from this one on
+  __device__ __forceinline__ rsrc_t take(int left) {
+    const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(base, 0, left > 1 ? kPastEnd : (left == 1 ? tail : 0), kBufWord3);
+    base += step;
+    return r;
+  }
+};
+
+template <int DK> struct DeltaWalkLds {
+  __attribute__((aligned(16))) uint16_t k[kDeltaC * kRowLd<DK>];
+  __attribute__((aligned(16))) uint16_t q[kDeltaC * kRowLd<DK>];
   __attribute__((aligned(16))) char img[kImgBytes];
 };
 
 template <int DK, int W, int NC>
 __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) {
   constexpr int KT = DK / 32, DT = DK / 16, NTH = 64 * W;
-  using Lds = DeltaWalkLds<DK, W, NC>;
-  constexpr int SP = Lds::SP, ST = Lds::ST;
+  using Lds = DeltaWalkLds<DK>;
   __shared__ Lds lds[2];
+  // each wavefront's own values, [token][channel], as they are in memory (bf16): written with the next chunk's
+  // operands, read transposed at its start
+  __shared__ __attribute__((aligned(16))) uint16_t lds_v[W][NC][kDeltaC * 16];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t blocks = (p.P + 16 * NC * W - 1) / (16 * NC * W);  // workgroups per unit
@@ -43,6 +67,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
   const DeltaSeq sq = delta_seq(p.cu, seq, p.L, p.chunks);
   const int nchunks = static_cast<int>((sq.len + kDeltaC - 1) / kDeltaC);
   const int64_t rowe = p.H * p.P, krow = p.G * DK;
+  const int rowe32 = static_cast<int>(rowe), krow32 = static_cast<int>(krow);  // the host keeps them below 2^22
+  const int yrow = (lr * rowe32 + 4 * lq) * 2;
 
   // ---- the state: channel col + 16 n + lr, states 16 d + 4 lq .. + 3
   f32x4_t S[NC][DT];
@@ -57,85 +83,94 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
     }
 
   // ---- chunk loads, one chunk ahead in registers
-  constexpr int PER = kDeltaC * DK / 8 / NTH;
-  constexpr int IPER = (kImgBytes / 16 + NTH - 1) / NTH;
-  u32x4_t gk[PER], gq[PER], gi[IPER];
-  uint16_t gv[NC][4][4];
-  auto load = [&](int c) {
-    const int64_t c0 = static_cast<int64_t>(c) * kDeltaC, tok = sq.tok + c0;
-    const int nt = static_cast<int>(sq.len - c0 < kDeltaC ? sq.len - c0 : kDeltaC);
-    const int64_t kb = tok * krow + g * DK, kbytes = ((nt - 1) * krow + DK) * 2;
-    const rsrc_t rk = make_rsrc(static_cast<const uint16_t*>(p.k) + kb, kbytes);
-    const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(p.q) + kb, kbytes);
+  constexpr int PIECES = kDeltaC * DK / 8, PER = (PIECES + NTH - 1) / NTH;
+  constexpr int IPIECES = kImgBytes / 16, IPER = (IPIECES + NTH - 1) / NTH;
+  // byte offset of the channel tile: past every resource when the head has no such tile, where loads return zero and
+  // stores are dropped (a branch around each load would make the compiler wait for it)
+  int ctile[NC];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = tid + NTH * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
-      const int off = static_cast<int>((row * krow + cc) * 2);
+  for (int n = 0; n < NC; ++n) ctile[n] = col + 16 * n < p.P ? (col + 16 * n) * 2 : kPastEnd;
+  u32x4_t gk[PER], gq[PER], gi[IPER];
+  u32x2_t gv[NC][4];
+  // Each tensor's chunks in order, as a base that moves on (computing a chunk's address anew took a hundred scalar
+  // instructions a chunk).  Past the last chunk the resources are empty, so the loop loads without a branch: a
+  // conditional load's registers would be copied, and waited for, where the paths meet.
+  const int64_t kb = sq.tok * krow + g * DK, vb = sq.tok * rowe + h * p.P;
+  const int64_t last = sq.len - static_cast<int64_t>(nchunks - 1) * kDeltaC;  // tokens of the last chunk
+  const int64_t ktail = ((last - 1) * krow + DK) * 2, vtail = ((last - 1) * rowe + p.P) * 2;
+  DeltaStream ks(static_cast<const uint16_t*>(p.k) + kb, krow * kDeltaC * 2, ktail);
+  DeltaStream qs(static_cast<const uint16_t*>(p.q) + kb, krow * kDeltaC * 2, ktail);
+  DeltaStream vs(static_cast<const uint16_t*>(p.v) + vb, rowe * kDeltaC * 2, vtail);
+  DeltaStream ys(static_cast<uint16_t*>(p.y) + vb, rowe * kDeltaC * 2, vtail);
+  DeltaStream is(p.img + (sq.slot * p.H + h) * kImgBytes, p.H * kImgBytes, kImgBytes);
+  // y of a chunk, four consecutive channels of token 16 t + lr in a lane; stored during the chunk after it
+  u32x2_t yo[NC][4];
+  // What passes between memory, registers and LDS for a chunk, as ITEMS: the row pieces of K and Q, the image's
+  // pieces, the values and y, two token tiles each.  A step of the loop below takes its share of them: piece by piece
+  // into LDS what was loaded a chunk ago, and the same piece of the chunk after out of memory.  (All at once they
+  // kept the wavefronts waiting for the CU's one memory path: 64 bytes a clock for 83 KB a chunk.)
+  constexpr int ITEMS = PER + IPER + 4 * NC;
+  rsrc_t rk, rq, ri, rv, ry;
+  auto next_rsrc = [&](int left) { rk = ks.take(left), rq = qs.take(left), ri = is.take(left), rv = vs.take(left); };
+  auto load_item = [&](auto item) {
+    constexpr int i = decltype(item)::value;
+    if constexpr (i < PER) {
+      const int e = tid + NTH * i;
+      const int off = (e / (DK / 8)) * krow32 * 2 + (e % (DK / 8)) * 16;
       gk[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0));
       gq[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
+    } else if constexpr (i < PER + IPER) {
+      constexpr int e = i - PER;
+      gi[e] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ri, (tid + NTH * e) * 16, 0, 0));
+    } else if constexpr (i < PER + IPER + 2 * NC) {
+      constexpr int n = (i - PER - IPER) / 2, t = 2 * ((i - PER - IPER) % 2);
+      const int at = yrow + ctile[n];
+      gv[n][t] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rv, at, 32 * t * rowe32, 0));
+      gv[n][t + 1] =
+          __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rv, at, 32 * (t + 1) * rowe32, 0));
     }
-    const u32x4_t* im = reinterpret_cast<const u32x4_t*>(p.img + ((sq.slot + c) * p.H + h) * kImgBytes);
-#pragma unroll
-    for (int i = 0; i < IPER; ++i) {
-      const int e = tid + NTH * i;
-      if (e < kImgBytes / 16) gi[i] = im[e];
-    }
-    // rows behind the sequence's end read as zero
-    const rsrc_t rv = make_rsrc(static_cast<const uint16_t*>(p.v) + tok * rowe + h * p.P, ((nt - 1) * rowe + p.P) * 2);
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          gv[n][t][r] = 0;
-          if (col + 16 * n < p.P)
-            gv[n][t][r] = __builtin_amdgcn_raw_buffer_load_b16(
-                rv, static_cast<int>(((16 * t + 4 * lq + r) * rowe + col + 16 * n + lr) * 2), 0, 0);
-        }
   };
-  auto stage = [&](Lds& b) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
+  auto stage_item = [&](Lds& b, auto item) {
+    constexpr int i = decltype(item)::value;
+    if constexpr (i < PER) {
       const int e = tid + NTH * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
-      const u32x4_t k8 = bf16x8_as_f16(gk[i]), q8 = bf16x8_as_f16(gq[i]);
-      const int j = (cc >> 2) & 7, blk = cc & ~31;  // this piece's runs j, j + 1 of its 32-element block
-      uint16_t* kp = &b.k[row * SP + blk];
-      uint16_t* qp = &b.q[row * SP + blk];
-      *reinterpret_cast<u32x2_t*>(kp + 4 * paired_run(j)) = u32x2_t{k8[0], k8[1]};
-      *reinterpret_cast<u32x2_t*>(kp + 4 * paired_run(j + 1)) = u32x2_t{k8[2], k8[3]};
-      *reinterpret_cast<u32x2_t*>(qp + 4 * paired_run(j)) = u32x2_t{q8[0], q8[1]};
-      *reinterpret_cast<u32x2_t*>(qp + 4 * paired_run(j + 1)) = u32x2_t{q8[2], q8[3]};
-      *reinterpret_cast<u32x4_t*>(&b.kt[row * ST + cc]) = k8;
-    }
-#pragma unroll
-    for (int i = 0; i < IPER; ++i) {
-      const int e = tid + NTH * i;
-      if (e < kImgBytes / 16) *reinterpret_cast<u32x4_t*>(&b.img[e * 16]) = gi[i];
+      // (a piece behind the 64 rows was loaded as zero and has no place)
+      if (PIECES % NTH == 0 || e < PIECES) {
+        *reinterpret_cast<u32x4_t*>(&b.k[row * kRowLd<DK> + cc]) = bf16x8_as_f16(gk[i]);
+        *reinterpret_cast<u32x4_t*>(&b.q[row * kRowLd<DK> + cc]) = bf16x8_as_f16(gq[i]);
+      }
+    } else if constexpr (i < PER + IPER) {
+      const int e = tid + NTH * (i - PER);
+      if (IPIECES % NTH == 0 || e < IPIECES) *reinterpret_cast<u32x4_t*>(&b.img[e * 16]) = gi[i - PER];
+    } else if constexpr (i < PER + IPER + 2 * NC) {
+      constexpr int n = (i - PER - IPER) / 2, t = 2 * ((i - PER - IPER) % 2);
+      *reinterpret_cast<u32x2_t*>(&lds_v[w][n][(16 * t + lr) * 16 + 4 * lq]) = gv[n][t];
+      *reinterpret_cast<u32x2_t*>(&lds_v[w][n][(16 * t + 16 + lr) * 16 + 4 * lq]) = gv[n][t + 1];
+    } else {
+      constexpr int e = i - PER - IPER - 2 * NC, n = e / 2, t = 2 * (e % 2);
+      __builtin_amdgcn_raw_buffer_store_b64(yo[n][t], ry, yrow + ctile[n], 32 * t * rowe32, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(yo[n][t + 1], ry, yrow + ctile[n], 32 * (t + 1) * rowe32, 0);
     }
   };
 
   if (nchunks > 0) {
-    load(0);
-    stage(lds[0]);
+    next_rsrc(nchunks);
+    static_for<ITEMS - 2 * NC>([&](auto i) { load_item(i); });
+    next_rsrc(nchunks - 1);
+    static_for<ITEMS - 2 * NC>([&](auto i) {
+      stage_item(lds[0], i);
+      load_item(i);
+    });
   }
   __syncthreads();
+  f16x8_t Sh[NC][KT], Sl[NC][KT];
+#pragma unroll
+  for (int n = 0; n < NC; ++n)
+#pragma unroll
+    for (int kk = 0; kk < KT; ++kk) split_f16(S[n][2 * kk], S[n][2 * kk + 1], Sh[n][kk], Sl[n][kk]);
   for (int c = 0; c < nchunks; ++c) {
     const Lds& b = lds[c & 1];
-    const int64_t c0 = static_cast<int64_t>(c) * kDeltaC, tok = sq.tok + c0;
-    const int nt = static_cast<int>(sq.len - c0 < kDeltaC ? sq.len - c0 : kDeltaC);
-    float v[NC][4][4];
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[n][t][r] = __uint_as_float(static_cast<uint32_t>(gv[n][t][r]) << 16);
-    if (c + 1 < nchunks) load(c + 1);
-
-    auto row_frag = [&](const uint16_t* a, int t, int kk) {
-      return *reinterpret_cast<const f16x8_t*>(&a[(16 * t + lr) * SP + 32 * kk + 8 * lq]);
-    };
+    Lds& next = lds[(c + 1) & 1];
     auto img_frag = [&](int base, int f) {
       return *reinterpret_cast<const f16x8_t*>(&b.img[base + f * kFrag + lane * 16]);
     };
@@ -143,113 +178,168 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
       return *reinterpret_cast<const f32x4_t*>(&b.img[base + (16 * t + 4 * lq) * 4]);
     };
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    f16x8_t Sh[NC][KT], Sl[NC][KT];
+    // ---- X = V - diag(e^cs) K S0, and Q S0 (as its transpose) beside it.  Steps (t, kk) in a row; the fragments of
+    // step j + 3 are read before the products of step j.
+    constexpr int STEPS = 4 * KT;
+    f16x8_t kf[4], qf[4];
+    auto read_step = [&](int j) {
+      kf[j & 3] = lds_row_frag<DK>(b.k, 16 * (j / KT) + lr, j % KT, lq);
+      qf[j & 3] = lds_row_frag<DK>(b.q, 16 * (j / KT) + lr, j % KT, lq);
+    };
+    f16x8_t th[6], tl[6];
+    auto read_t = [&](int f) { th[f] = img_frag(kImgThi, f), tl[f] = img_frag(kImgTlo, f); };
+    u32x2_t vq[NC][4];
+    const float fade = *reinterpret_cast<const float*>(&b.img[kImgGrow + (kDeltaC - 1) * 4]);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) read_step(j);
 #pragma unroll
     for (int n = 0; n < NC; ++n)
 #pragma unroll
-      for (int kk = 0; kk < KT; ++kk) split_f16(S[n][2 * kk], S[n][2 * kk + 1], Sh[n][kk], Sl[n][kk]);
-
-    // ---- X = diag(b) (V - diag(e^cs) K S0), and Q S0 (as its transpose) beside it
-    f32x4_t x[NC][4], o[NC][4];
+      for (int t = 0; t < 4; ++t) vq[n][t] = lds_tr4(&lds_v[w][n][(16 * t + 4 * lq + (lr >> 2)) * 16 + 4 * (lr & 3)]);
+    __builtin_amdgcn_sched_barrier(0);
+    next_rsrc(nchunks - c - 2);
+    ry = ys.take(c > 0 ? 2 : 0);  // of the chunk before, which is whole
+    if (c == 0) ys.base -= ys.step;
+    // this chunk's share of ITEMS, in slots evenly spread over its products
+    constexpr int SLOTS = STEPS + 3 + 2 * KT;
+    auto slot = [&](auto place) {
+      constexpr int k = decltype(place)::value, i0 = k * ITEMS / SLOTS, i1 = (k + 1) * ITEMS / SLOTS;
+      static_for<i1 - i0>([&](auto i) {
+        stage_item(next, IC<i0 + decltype(i)::value>{});
+        load_item(IC<i0 + decltype(i)::value>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4_t x[NC][4], o[NC][4], grow[2];
+    f16x8_t Xh[NC][2], Xl[NC][2];
+    auto finish_x = [&](int t) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+      for (int n = 0; n < NC; ++n) {
+        const float v[4] = {bf16_lo(vq[n][t][0]), bf16_hi(vq[n][t][0]), bf16_lo(vq[n][t][1]), bf16_hi(vq[n][t][1])};
 #pragma unroll
-      for (int n = 0; n < NC; ++n) x[n][t] = o[n][t] = zero;
-#pragma unroll
-      for (int kk = 0; kk < KT; ++kk) {
-        const f16x8_t kf = row_frag(b.k, t, kk), qf = row_frag(b.q, t, kk);
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          x[n][t] = mfma_f16(kf, Sh[n][kk], x[n][t]);
-          x[n][t] = mfma_f16(kf, Sl[n][kk], x[n][t]);
-          o[n][t] = mfma_f16(Sh[n][kk], qf, o[n][t]);
-        }
+        for (int r = 0; r < 4; ++r) x[n][t][r] = __builtin_fmaf(-grow[t & 1][r], x[n][t][r], v[r]);
+        if (t & 1) split_f16(x[n][t - 1], x[n][t], Xh[n][t >> 1], Xl[n][t >> 1]);
       }
-      const f32x4_t grow = img_vec(kImgGrow, t), beta = img_vec(kImgBeta, t);
+    };
+    static_for<STEPS>([&](auto step) {
+      constexpr int j = decltype(step)::value, t = j / KT, kk = j % KT;
+      if constexpr (j + 3 < STEPS)
+        read_step(j + 3);
+      else
+        read_t(j + 3 - STEPS);
+      if (kk == KT - 1) grow[t & 1] = img_vec(kImgGrow, t);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+      for (int n = 0; n < NC; ++n) {
+        if (kk == 0) x[n][t] = o[n][t] = zero;
+        x[n][t] = mfma_f16(kf[j & 3], Sl[n][kk], x[n][t]);
+        o[n][t] = mfma_f16(Sh[n][kk], qf[j & 3], o[n][t]);
+        x[n][t] = mfma_f16(kf[j & 3], Sh[n][kk], x[n][t]);
+      }
+      if constexpr (kk == 0 && t > 0) finish_x(t - 1);
+      // the state itself (its operands are copies) fades here, out of the chain
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[n][t][r] = beta[r] * __builtin_fmaf(-grow[r], x[n][t][r], v[n][t][r]);
-    }
-    // ---- U = T X
+      for (int d = j * DT / STEPS; d < (j + 1) * DT / STEPS; ++d)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) S[n][d] *= fade;
+      slot(IC<j>{});
+    });
+    finish_x(3);
+    // ---- R = T X
+    __builtin_amdgcn_sched_barrier(0);
+    read_t(3);
+    read_t(4);
+    read_t(5);
+    f32x4_t left[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) left[t] = img_vec(kImgLeft, t);
+    f16x8_t kc[DT];  // K^T, a half of the tokens at a time
+#pragma unroll
+    for (int d = 0; d < DT; ++d) kc[d] = lds_col_frag<DK>(b.k, 0, d, lr, lq);
+    __builtin_amdgcn_sched_barrier(0);
     f32x4_t u[NC][4];
-    {
-      f16x8_t Xh[NC][2], Xl[NC][2];
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) split_f16(x[n][2 * m], x[n][2 * m + 1], Xh[n][m], Xl[n][m]);
+      for (int t = 0; t < 4; ++t) u[n][t] = zero;
+    auto t_product = [&](int t, int m, int i) {
+      const int f = frag_of(t, m);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int n = 0; n < NC; ++n) u[n][t] = mfma_f16(i == 2 ? tl[f] : th[f], i == 1 ? Xl[n][m] : Xh[n][m], u[n][t]);
+    };
+    static_for<3>([&](auto i) {
+      t_product(0, 0, i.value);
+      t_product(1, 0, i.value);
+      t_product(2, 0, i.value);
+      t_product(3, 0, i.value);
+      slot(IC<STEPS + decltype(i)::value>{});
+    });
+    // ---- S = e^{cs_C} S + K^T diag(e^{cs_C - cs} b) R
+    f16x8_t Uh[NC][2], Ul[NC][2];
+    static_for<3>([&](auto i) {
+      t_product(2, 1, i.value);
+      t_product(3, 1, i.value);
+    });
 #pragma unroll
-        for (int n = 0; n < NC; ++n) u[n][t] = zero;
+    for (int n = 0; n < NC; ++n) split_f16(u[n][0] * left[0], u[n][1] * left[1], Uh[n][0], Ul[n][0]);
+    auto state_product = [&](int d, int m) {
 #pragma unroll
-        for (int m = 0; m <= t / 2; ++m) {
-          const f16x8_t th = img_frag(kImgThi, frag_of(t, m)), tl = img_frag(kImgTlo, frag_of(t, m));
-#pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            u[n][t] = mfma_f16(th, Xh[n][m], u[n][t]);
-            u[n][t] = mfma_f16(th, Xl[n][m], u[n][t]);
-            u[n][t] = mfma_f16(tl, Xh[n][m], u[n][t]);
-          }
-        }
+      for (int n = 0; n < NC; ++n) {
+        S[n][d] = mfma_f16(kc[d], Uh[n][m], S[n][d]);
+        S[n][d + 1] = mfma_f16(kc[d + 1], Uh[n][m], S[n][d + 1]);
+        S[n][d] = mfma_f16(kc[d], Ul[n][m], S[n][d]);
+        S[n][d + 1] = mfma_f16(kc[d + 1], Ul[n][m], S[n][d + 1]);
       }
+    };
+    static_for<KT>([&](auto k) {
+      constexpr int d = 2 * decltype(k)::value;
+      state_product(d, 0);
+      kc[d] = lds_col_frag<DK>(b.k, 32, d, lr, lq);
+      kc[d + 1] = lds_col_frag<DK>(b.k, 32, d + 1, lr, lq);
+      slot(IC<STEPS + 3 + decltype(k)::value>{});
+    });
+    f16x8_t Rf[NC][2];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      split_f16(u[n][2] * left[2], u[n][3] * left[3], Uh[n][1], Ul[n][1]);
+      Rf[n][0] = pair_f16(u[n][0], u[n][1]), Rf[n][1] = pair_f16(u[n][2], u[n][3]);
     }
-    // ---- S = e^{cs_C} S + K^T diag(e^{cs_C - cs}) U
-    {
-      const float fade = *reinterpret_cast<const float*>(&b.img[kImgGrow + (kDeltaC - 1) * 4]);
+    f16x8_t pf[6];
+    float og[4];
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+    for (int t = 0; t < 4; ++t) og[t] = *reinterpret_cast<const float*>(&b.img[kImgOut + (16 * t + lr) * 4]);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) S[n][d] *= fade;
+    for (int f = 0; f < 6; ++f) pf[f] = img_frag(kImgP, f);
+    __builtin_amdgcn_sched_barrier(0);
+    // the next chunk's operands of the state are split under the products of the following tiles
+    static_for<KT>([&](auto k) {
+      constexpr int kk = decltype(k)::value, d = 2 * kk;
+      state_product(d, 1);
+      if constexpr (kk > 0) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        f16x8_t Uh[NC], Ul[NC];
-        const f32x4_t l0 = img_vec(kImgLeft, 2 * m), l1 = img_vec(kImgLeft, 2 * m + 1);
-#pragma unroll
-        for (int n = 0; n < NC; ++n) split_f16(u[n][2 * m] * l0, u[n][2 * m + 1] * l1, Uh[n], Ul[n]);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const f16x8_t kf = lds_col_frag(b.kt, 32 * m, 16 * d, ST, lr, lq);
-#pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            S[n][d] = mfma_f16(kf, Uh[n], S[n][d]);
-            S[n][d] = mfma_f16(kf, Ul[n], S[n][d]);
-          }
-        }
+        for (int n = 0; n < NC; ++n) split_f16(S[n][d - 2], S[n][d - 1], Sh[n][kk - 1], Sl[n][kk - 1]);
       }
+      slot(IC<STEPS + 3 + KT + kk>{});
+    });
+    // ---- Y^T = (Q S0)^T diag(scale e^cs) + R^T P^T
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[n][t] *= og[t];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[n][t] = mfma_f16(Rf[n][0], pf[frag_of(t, 0)], o[n][t]);
+#pragma unroll
+      for (int t = 2; t < 4; ++t) o[n][t] = mfma_f16(Rf[n][1], pf[frag_of(t, 1)], o[n][t]);
+      split_f16(S[n][DT - 2], S[n][DT - 1], Sh[n][KT - 1], Sl[n][KT - 1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        yo[n][t] = u32x2_t{pack_bf16x2(o[n][t][0], o[n][t][1]), pack_bf16x2(o[n][t][2], o[n][t][3])};
     }
-    // ---- Y^T = scale (e^cs (Q S0)^T + U^T P^T): four consecutive channels of token 16 t + lr in a lane
-    {
-      f16x8_t Uf[NC][2];
-#pragma unroll
-      for (int n = 0; n < NC; ++n)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) Uf[n][m] = pair_f16(u[n][2 * m], u[n][2 * m + 1]);
-      const rsrc_t ry = make_rsrc(static_cast<uint16_t*>(p.y) + tok * rowe + h * p.P, ((nt - 1) * rowe + p.P) * 2);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float grow = *reinterpret_cast<const float*>(&b.img[kImgGrow + (16 * t + lr) * 4]);
-#pragma unroll
-        for (int n = 0; n < NC; ++n) o[n][t] *= grow;
-#pragma unroll
-        for (int m = 0; m <= t / 2; ++m) {
-          const f16x8_t pf = img_frag(kImgP, frag_of(t, m));
-#pragma unroll
-          for (int n = 0; n < NC; ++n) o[n][t] = mfma_f16(Uf[n][m], pf, o[n][t]);
-        }
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          o[n][t] *= p.scale;
-          if (col + 16 * n < p.P)
-            __builtin_amdgcn_raw_buffer_store_b64(
-                u32x2_t{pack_bf16x2(o[n][t][0], o[n][t][1]), pack_bf16x2(o[n][t][2], o[n][t][3])}, ry,
-                static_cast<int>(((16 * t + lr) * rowe + col + 16 * n + 4 * lq) * 2), 0, 0);
-        }
-      }
-    }
-    if (c + 1 < nchunks) stage(lds[(c + 1) & 1]);
     __syncthreads();
+  }
+  if (nchunks > 0) {
+    ry = ys.take(1);
+    static_for<2 * NC>([&](auto i) { stage_item(lds[0], IC<ITEMS - 2 * NC + decltype(i)::value>{}); });
   }
   if (p.hT) {
 #pragma unroll

@@ -70,8 +70,8 @@ DeltaStepParams step_params(const DeltaArgs& a) {
 // ---- the chunked plan
 bool delta_chunked(int64_t L, int64_t heads, int64_t headdim, int64_t dstate, int64_t nseq, ssm_dtype_t dt) {
   if (dt != SSM_DTYPE_BF16 || dstate > 128 || headdim % 16 != 0) return false;
-  // a chunk's rows are addressed with 32-bit byte offsets
-  if (heads * headdim > (1 << 23) || heads * dstate > (1 << 23)) return false;
+  // a chunk's 64 rows, and as much again behind them, are addressed with 32-bit byte offsets
+  if (heads * headdim > (1 << 22) || heads * dstate > (1 << 22)) return false;
   const char* e = getenv("SSM_DELTA_CHUNKED");
   if (e) return atoi(e) != 0;
   return L / (nseq > 0 ? nseq : 1) > 16;
@@ -87,13 +87,18 @@ template <int DK> hipError_t run_chunked(DeltaChunkParams& p, hipStream_t s) {
   hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t tiles = p.P / 16;
-  if (tiles > 4) {
-    const int64_t wgs = p.rows * p.H * ((tiles + 7) / 8);
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 2>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, s, p);
+  const int64_t tiles = p.P / 16, units = p.rows * p.H;
+  const char* ev = getenv("SSM_DELTA_WALK");
+  const int v = ev ? atoi(ev) : 0;
+  if (tiles > 4 && v == 81) {
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 8, 1>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))), dim3(512),
+                       0, s, p);
+  } else if (tiles > 4 && v != 41) {
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 2>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))), dim3(256),
+                       0, s, p);
   } else {
-    const int64_t wgs = p.rows * p.H * ((tiles + 3) / 4);
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 1>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 1>), dim3(static_cast<unsigned>(units * ((tiles + 3) / 4))), dim3(256),
+                       0, s, p);
   }
   return hipGetLastError();
 }
