@@ -95,18 +95,26 @@ __device__ __forceinline__ u32x4_t bf16x8_as_f16(u32x4_t v) {
   return r;
 }
 
-// K and Q of a chunk in LDS: fp16 rows of DK elements, 4 x odd dwords apart.
-// Sixteen rows x two neighbouring 8-byte runs (a fragment of rows: two runs 32
-// bytes apart a lane, one read of 2 x 8 bytes) then touch every bank once, and
-// the transposed reads of a fragment of columns (eight rows x 32 bytes) every
-// bank twice.  (An 8 x odd stride turns that round; a swizzle that serves both
-// needs an address register per fragment, which the walk does not have.)
+// K and Q of a chunk in LDS, fp16.  For fragments of rows (16 rows x 32
+// columns) each 32-element block is stored in paired order, so that a lane
+// reads its two runs with one 16-byte read (two 8-byte runs in one instruction
+// take twice as long), rows 4 x odd dwords apart: every bank once.  For
+// fragments of columns (transposed reads, eight rows x 32 bytes at a time) K
+// is kept a second time, as it is, rows 8 x odd dwords apart: every bank once.
 template <int DK> constexpr int kRowLd = DK + 8;
-// 32 K indices from 32 kk of row r in paired order (this lane: runs lq and lq + 4).
+template <int DK> constexpr int kColLd = DK + 16;
+// Where run j (four elements) of a 32-element block sits in paired order.
+__device__ __forceinline__ constexpr int paired_run(int j) { return j < 4 ? 2 * j : 2 * j - 7; }
+// Elements cc .. cc + 7 (cc a multiple of 8) of a row in paired order.
+__device__ __forceinline__ void lds_store_paired(uint16_t* row, int cc, u32x4_t v) {
+  uint16_t* a = row + (cc & ~31);
+  const int j = (cc >> 2) & 7;
+  *reinterpret_cast<u32x2_t*>(a + 4 * paired_run(j)) = u32x2_t{v[0], v[1]};
+  *reinterpret_cast<u32x2_t*>(a + 4 * paired_run(j + 1)) = u32x2_t{v[2], v[3]};
+}
+// Columns 32 kk .. + 31 of row r.
 template <int DK> __device__ __forceinline__ f16x8_t lds_row_frag(const uint16_t* base, int r, int kk, int lq) {
-  const uint16_t* a = base + r * kRowLd<DK> + 32 * kk + 4 * lq;
-  const u32x2_t x = *reinterpret_cast<const u32x2_t*>(a), y = *reinterpret_cast<const u32x2_t*>(a + 16);
-  return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
+  return *reinterpret_cast<const f16x8_t*>(base + r * kRowLd<DK> + 32 * kk + 8 * lq);
 }
 // Transposed LDS read (ds_read_b64_tr_b16): lane i of 16 receives, of the four
 // rows that the 16 lanes address as 4 x 4 runs (lane i: row i / 4, run i % 4),
@@ -118,8 +126,8 @@ __device__ __forceinline__ u32x2_t lds_tr4(const uint16_t* a) {
 }
 // A fragment whose K index is the row of such an array: rows k0 .. k0 + 31 in paired order, columns 16 d + lr.
 template <int DK> __device__ __forceinline__ f16x8_t lds_col_frag(const uint16_t* base, int k0, int d, int lr, int lq) {
-  const uint16_t* a = base + (k0 + 4 * lq + (lr >> 2)) * kRowLd<DK> + 16 * d + 4 * (lr & 3);
-  const u32x2_t x = lds_tr4(a), y = lds_tr4(a + 16 * kRowLd<DK>);
+  const uint16_t* a = base + (k0 + 4 * lq + (lr >> 2)) * kColLd<DK> + 16 * d + 4 * (lr & 3);
+  const u32x2_t x = lds_tr4(a), y = lds_tr4(a + 16 * kColLd<DK>);
   return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
 }
 

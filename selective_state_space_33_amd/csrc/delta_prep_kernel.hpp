@@ -4,12 +4,15 @@
 //
 // One workgroup of four wavefronts per (chunk, head).  K and Q of the chunk
 // sit in LDS as they come (bf16, so the products K K^T and K Q^T are exact up
-// to their fp32 sums).  cs is summed in fp64 and kept as a pair of floats:
-// differences of neighbours deep in a fast-fading chunk would otherwise lose
-// bits.  The inverse is a forward substitution: the four 16 x 16 diagonal
-// blocks at once in one wavefront (a lane a column), then block column j in
-// wavefront j, T_ij = -T_ii sum_l M_il T_lj, on fp32 MFMA (16x16x4), whose
-// accumulators again serve as the next product's operand.
+// to their fp32 sums); each wavefront forms a row of M tiles and a column of P
+// tiles, five in all, then M takes K's place (35 KB a workgroup: four of them
+// share a CU, which hides their serial parts).  cs is summed in fp64 and kept
+// as a pair of floats: differences of neighbours deep in a fast-fading chunk
+// would otherwise lose bits.  The inverse is a forward substitution: the four
+// 16 x 16 diagonal blocks at once in one wavefront (a lane a column), then
+// block column j in wavefront j, T_ij = -T_ii sum_l M_il T_lj, on fp32 MFMA
+// (16x16x4), whose accumulators again serve as the next product's operand.
+// T replaces M block by block: T_ii in place, T_ij in the unused block (j, i).
 #pragma once
 
 #include "delta_chunk.hpp"
@@ -27,29 +30,32 @@ __device__ __forceinline__ f32x4_t mfma_f32_tile(const float* a, f32x4_t b, f32x
   return acc;
 }
 
-// Block column J of T from the diagonal blocks in sT, written to sT.
-template <int J> __device__ __forceinline__ void prep_column(const float* sM, float* sT, int lr, int lq) {
+// Block column J of T; sM holds M below the diagonal and the T_ii on it.
+template <int J> __device__ __forceinline__ void prep_column(float* sM, int lr, int lq) {
   f32x4_t t[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) t[J][r] = sT[(16 * J + 4 * lq + r) * kPrepLd + 16 * J + lr];
+  for (int r = 0; r < 4; ++r) t[J][r] = sM[(16 * J + 4 * lq + r) * kPrepLd + 16 * J + lr];
 #pragma unroll
   for (int i = J + 1; i < 4; ++i) {
     f32x4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int l = J; l < i; ++l) z = mfma_f32_tile(&sM[(16 * i + lr) * kPrepLd + 16 * l + 4 * lq], t[l], z);
-    t[i] = mfma_f32_tile(&sT[(16 * i + lr) * kPrepLd + 16 * i + 4 * lq], z, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+    t[i] = mfma_f32_tile(&sM[(16 * i + lr) * kPrepLd + 16 * i + 4 * lq], z, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       t[i][r] = -t[i][r];
-      sT[(16 * i + 4 * lq + r) * kPrepLd + 16 * J + lr] = t[i][r];
+      sM[(16 * J + 4 * lq + r) * kPrepLd + 16 * i + lr] = t[i][r];  // in block (J, i)
     }
   }
 }
 
 template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkParams p) {
   constexpr int SB = DK + 8;  // bf16 row stride
-  __shared__ __attribute__((aligned(16))) uint16_t sK[kDeltaC * SB], sQ[kDeltaC * SB];
-  __shared__ __attribute__((aligned(16))) float sM[kDeltaC * kPrepLd], sT[kDeltaC * kPrepLd];
+  constexpr int ROWS = 2 * kDeltaC * SB * 2, MAT = kDeltaC * kPrepLd * 4;  // bytes
+  __shared__ __attribute__((aligned(16))) char sMem[ROWS > MAT ? ROWS : MAT];
+  uint16_t* const sK = reinterpret_cast<uint16_t*>(sMem);
+  uint16_t* const sQ = sK + kDeltaC * SB;
+  float* const sM = reinterpret_cast<float*>(sMem);
   __shared__ __attribute__((aligned(16))) float sChi[kDeltaC], sClo[kDeltaC], sBeta[kDeltaC];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
@@ -135,18 +141,54 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
     return __builtin_amdgcn_exp2f(((sChi[t] - sChi[j]) + (sClo[t] - sClo[j])) * kLog2e);
   };
   // ---- M = N diag(b): row tile w, column tiles 0 .. w
-  for (int jt = 0; jt <= w; ++jt) {
-    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4_t m[4];
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt) {
+    m[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (jt > w) continue;
 #pragma unroll
     for (int kk = 0; kk < DK / 32; ++kk)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, w, kk), frag(sK, jt, kk), acc, 0, 0, 0);
+      m[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, w, kk), frag(sK, jt, kk), m[jt], 0, 0, 0);
     const int j = 16 * jt + lr;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * w + 4 * lq + r;
-      sM[t * kPrepLd + j] = j < t ? sBeta[j] * fade(t, j) * acc[r] : 0.0f;
+      m[jt][r] = j < t ? sBeta[j] * fade(t, j) * m[jt][r] : 0.0f;
     }
   }
+  // ---- P: the tiles of K Q^T leave four consecutive j of token t = lr in a lane, half a fragment
+  {
+    const int tt = 3 - w, t = 16 * tt + lr;
+    for (int m2 = 0; m2 <= tt / 2; ++m2) {
+      f32x4_t half[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int jt = 2 * m2 + u;
+        f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (jt <= tt) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 32; ++kk)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, jt, kk), frag(sQ, tt, kk), acc, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = 16 * jt + 4 * lq + r;
+            acc[r] = j <= t ? p.scale * sBeta[j] * fade(t, j) * acc[r] : 0.0f;
+          }
+        }
+        half[u] = acc;
+      }
+      // fp16: P meets R (fp16 too) in y alone, which is stored with 8 significant bits
+      *reinterpret_cast<f16x8_t*>(p.img + id * kImgBytes + kImgP + frag_of(tt, m2) * kFrag + lane * 16) =
+          pair_f16(half[0], half[1]);
+    }
+  }
+  __syncthreads();  // K and Q are read
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt)
+    if (jt <= w) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sM[(16 * w + 4 * lq + r) * kPrepLd + 16 * jt + lr] = m[jt][r];
+    }
   __syncthreads();
   if (w == 0) {
     // ---- the diagonal blocks' inverses: lane (block, column c) solves (I + M_bb) x = e_c
@@ -157,59 +199,35 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
       float acc0 = i == c ? 1.0f : 0.0f, acc1 = 0.0f;
 #pragma unroll
       for (int j = 0; j < i; ++j) {
-        const float m = sM[(b0 + i) * kPrepLd + b0 + j];
+        const float mv = sM[(b0 + i) * kPrepLd + b0 + j];
         if (j & 1)
-          acc1 = __builtin_fmaf(-m, x[j], acc1);
+          acc1 = __builtin_fmaf(-mv, x[j], acc1);
         else
-          acc0 = __builtin_fmaf(-m, x[j], acc0);
+          acc0 = __builtin_fmaf(-mv, x[j], acc0);
       }
       x[i] = acc0 + acc1;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sT[(b0 + i) * kPrepLd + b0 + c] = x[i];
-  } else {
-    // ---- P meanwhile: the tiles of K Q^T leave four consecutive j of token t = lr in a lane, half a fragment
-    const int first = w == 1 ? 3 : (w == 2 ? 2 : 0), last = w == 3 ? 1 : first;
-    for (int tt = first; tt <= last; ++tt) {
-      for (int m = 0; m <= tt / 2; ++m) {
-        f32x4_t half[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int jt = 2 * m + u, t = 16 * tt + lr;
-          f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (jt <= tt) {
-#pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk)
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, jt, kk), frag(sQ, tt, kk), acc, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int j = 16 * jt + 4 * lq + r;
-              acc[r] = j <= t ? p.scale * sBeta[j] * fade(t, j) * acc[r] : 0.0f;
-            }
-          }
-          half[u] = acc;
-        }
-        // fp16: P meets R (fp16 too) in y alone, which is stored with 8 significant bits
-        *reinterpret_cast<f16x8_t*>(p.img + id * kImgBytes + kImgP + frag_of(tt, m) * kFrag + lane * 16) =
-            pair_f16(half[0], half[1]);
-      }
-    }
+    for (int i = 0; i < 16; ++i) sM[(b0 + i) * kPrepLd + b0 + c] = x[i];
   }
   __syncthreads();
   if (w == 0)
-    prep_column<0>(sM, sT, lr, lq);
+    prep_column<0>(sM, lr, lq);
   else if (w == 1)
-    prep_column<1>(sM, sT, lr, lq);
+    prep_column<1>(sM, lr, lq);
   else if (w == 2)
-    prep_column<2>(sM, sT, lr, lq);
+    prep_column<2>(sM, lr, lq);
   __syncthreads();
   // ---- T as fragments, hi + lo
   for (int e = tid; e < 6 * 64; e += 256) {
     const int f = e >> 6, ln = e & 63, row = ln & 15, q4 = 4 * (ln >> 4);
     const int t = f < 2 ? f : 2 + ((f - 2) >> 1), m = f < 2 ? 0 : (f & 1);
-    const float* a = &sT[(16 * t + row) * kPrepLd + 32 * m + q4];
-    const f32x4_t x0 = *reinterpret_cast<const f32x4_t*>(a);
-    const f32x4_t x1 = 2 * m + 1 <= t ? *reinterpret_cast<const f32x4_t*>(a + 16) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    // block (t, j) of T sits at (t, t), or at (j, t) for j < t
+    auto block = [&](int j) {
+      return *reinterpret_cast<const f32x4_t*>(&sM[(16 * (j < t ? j : t) + row) * kPrepLd + 16 * t + q4]);
+    };
+    const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    const f32x4_t x0 = block(2 * m), x1 = 2 * m + 1 <= t ? block(2 * m + 1) : zero;
     f16x8_t hi, lo;
     split_f16(x0, x1, hi, lo);
     char* out = p.img + id * kImgBytes + f * kFrag + ln * 16;

@@ -46,6 +46,7 @@ struct DeltaStream {
 
 template <int DK> struct DeltaWalkLds {
   __attribute__((aligned(16))) uint16_t k[kDeltaC * kRowLd<DK>];
+  __attribute__((aligned(16))) uint16_t kt[kDeltaC * kColLd<DK>];
   __attribute__((aligned(16))) uint16_t q[kDeltaC * kRowLd<DK>];
   __attribute__((aligned(16))) char img[kImgBytes];
 };
@@ -136,8 +137,10 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
       const int e = tid + NTH * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
       // (a piece behind the 64 rows was loaded as zero and has no place)
       if (PIECES % NTH == 0 || e < PIECES) {
-        *reinterpret_cast<u32x4_t*>(&b.k[row * kRowLd<DK> + cc]) = bf16x8_as_f16(gk[i]);
-        *reinterpret_cast<u32x4_t*>(&b.q[row * kRowLd<DK> + cc]) = bf16x8_as_f16(gq[i]);
+        const u32x4_t k8 = bf16x8_as_f16(gk[i]), q8 = bf16x8_as_f16(gq[i]);
+        lds_store_paired(&b.k[row * kRowLd<DK>], cc, k8);
+        *reinterpret_cast<u32x4_t*>(&b.kt[row * kColLd<DK> + cc]) = k8;
+        lds_store_paired(&b.q[row * kRowLd<DK>], cc, q8);
       }
     } else if constexpr (i < PER + IPER) {
       const int e = tid + NTH * (i - PER);
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
     for (int t = 0; t < 4; ++t) left[t] = img_vec(kImgLeft, t);
     f16x8_t kc[DT];  // K^T, a half of the tokens at a time
 #pragma unroll
-    for (int d = 0; d < DT; ++d) kc[d] = lds_col_frag<DK>(b.k, 0, d, lr, lq);
+    for (int d = 0; d < DT; ++d) kc[d] = lds_col_frag<DK>(b.kt, 0, d, lr, lq);
     __builtin_amdgcn_sched_barrier(0);
     f32x4_t u[NC][4];
 #pragma unroll
@@ -294,8 +297,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
     static_for<KT>([&](auto k) {
       constexpr int d = 2 * decltype(k)::value;
       state_product(d, 0);
-      kc[d] = lds_col_frag<DK>(b.k, 32, d, lr, lq);
-      kc[d + 1] = lds_col_frag<DK>(b.k, 32, d + 1, lr, lq);
+      kc[d] = lds_col_frag<DK>(b.kt, 32, d, lr, lq);
+      kc[d + 1] = lds_col_frag<DK>(b.kt, 32, d + 1, lr, lq);
       slot(IC<STEPS + 3 + decltype(k)::value>{});
     });
     f16x8_t Rf[NC][2];

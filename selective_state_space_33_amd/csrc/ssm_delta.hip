@@ -88,18 +88,14 @@ template <int DK> hipError_t run_chunked(DeltaChunkParams& p, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t tiles = p.P / 16, units = p.rows * p.H;
-  const char* ev = getenv("SSM_DELTA_WALK");
-  const int v = ev ? atoi(ev) : 0;
-  if (tiles > 4 && v == 81) {
+  // Four wavefronts a workgroup while every workgroup gets a CU of its own (a SIMD is then one wavefront's: dstate 128
+  // 2.8 us a chunk), else eight, which share a head's staging (3.4 us a chunk for twice the channels).
+  const int64_t small = units * ((tiles + 3) / 4);
+  if (tiles > 4 && small > device_cu_count())
     hipLaunchKernelGGL((delta_walk_kernel<DK, 8, 1>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))), dim3(512),
                        0, s, p);
-  } else if (tiles > 4 && v != 41) {
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 2>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))), dim3(256),
-                       0, s, p);
-  } else {
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 1>), dim3(static_cast<unsigned>(units * ((tiles + 3) / 4))), dim3(256),
-                       0, s, p);
-  }
+  else
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 1>), dim3(static_cast<unsigned>(small)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
