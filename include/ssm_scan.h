@@ -432,6 +432,41 @@ ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* v, const vo
 size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int64_t headdim, int64_t ngroups,
                                     int64_t dstate, int64_t nseq, ssm_dtype_t dt);
 
+/* Backward of ssm_delta_fwd: the gradients of
+ *     sum(y * dy) + sum(final_state * dfinal_state)
+ * for the same inputs and flags; states are recomputed, not stored by the
+ * forward.  dy [batch, L, heads, headdim] in dtype dt; dfinal_state (NULL: no
+ * gradient reaches the final states) and initial_state (NULL: zero) [rows,
+ * heads, headdim, dstate] fp32.
+ *   Outputs: dq, dk, dv, ddelta (of the raw step), dbeta (of the raw beta
+ *   when sigmoid_flag is set), shaped like their inputs, in dtype dt; dA
+ *   [heads] fp32; ddelta_bias [heads] fp32 (nullable) and dinitial_state
+ *   (nullable) like the states.  dq and dk sum over the heads of a group, dA
+ *   and ddelta_bias over the tokens, in a fixed order.  Packed sequences as
+ *   in ssm_delta_fwd: rows of no sequence are left as they were, and an empty
+ *   sequence hands dfinal_state to dinitial_state unchanged.
+ *   dt = BF16, dstate 32, 64, 96 or 128, headdim a multiple of 16, heads *
+ *   headdim and heads * dstate up to 2^22; else UNSUPPORTED.  q, k, v, dy, dv
+ *   and the states 16-byte aligned, everything else to its element.  Only
+ *   dfinal_state and dinitial_state may be the same buffer; no other output
+ *   may alias anything.  q, k, v and the states must stay below 65504 in
+ *   magnitude (ssm_delta_fwd); dy and dfinal_state may have any magnitude:
+ *   each (row, head) is scaled by a power of two of its own.  workspace:
+ *   ssm_delta_bwd_workspace_size() bytes, 256-byte aligned (at dstate =
+ *   headdim = 128 about 162 KB per chunk of 64 tokens and head). */
+ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
+                           const void* beta, const float* delta_bias, int softplus_flag, int sigmoid_flag,
+                           float scale, const void* dy, const float* dfinal_state, const float* initial_state,
+                           const int64_t* cu_seqlens, int64_t nseq, void* dq, void* dk, void* dv, void* ddelta,
+                           float* dA, void* dbeta, float* ddelta_bias, float* dinitial_state, int64_t batch,
+                           int64_t L, int64_t heads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                           ssm_dtype_t dt, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace ssm_delta_bwd needs; 0 for arguments it would
+ * reject. */
+size_t ssm_delta_bwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int64_t headdim, int64_t ngroups,
+                                    int64_t dstate, int64_t nseq, ssm_dtype_t dt);
+
 /* One decode step of the gated delta rule: one token of ssm_delta_fwd, in
  * fp32, reading `state` [batch, heads, headdim, dstate] as S_{t-1} and
  * overwriting it in place.  q, k: [batch, ngroups, dstate]; v, y: [batch,

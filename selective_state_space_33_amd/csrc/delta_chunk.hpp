@@ -49,6 +49,15 @@ constexpr int kImgGrow = 18 * kFrag;         // e^{cs_t}
 constexpr int kImgOut = kImgGrow + 256;      // scale e^{cs_t}
 constexpr int kImgLeft = kImgGrow + 512;     // e^{cs_C - cs_t} b_t (0 behind the sequence's end)
 constexpr int kImgBytes = kImgGrow + 768;
+// The backward's image: the same fragments of T, then P without b as a pair, and the gates.
+constexpr int kBwdPlo = 18 * kFrag;
+constexpr int kBwdGates = 24 * kFrag;
+constexpr int kBwdGrow = kBwdGates;          // e^{cs_t}
+constexpr int kBwdOut = kBwdGates + 256;     // scale e^{cs_t}
+constexpr int kBwdLeft = kBwdGates + 512;    // e^{cs_C - cs_t}
+constexpr int kBwdBeta = kBwdGates + 768;    // b_t
+constexpr int kBwdCs = kBwdGates + 1024;     // cs_t, as a pair of floats: hi, then lo
+constexpr int kBwdImgBytes = kBwdGates + 1536;
 __host__ __device__ constexpr int frag_of(int t, int m) { return t < 2 ? t : 2 + 2 * (t - 2) + m; }
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -162,6 +171,12 @@ __device__ __forceinline__ DeltaSeq delta_seq(const int64_t* cu, int64_t s, int6
   return d;
 }
 
+// A channel tile that the head does not have is addressed here: behind every
+// resource (they are cut to this length, and a chunk's offsets, 64 rows of at
+// most 2^23 bytes, stay below half of it), so loads return zero and stores are
+// dropped.
+constexpr int kPastEnd = 0x40000000;
+
 // Workgroups are dealt round-robin to the eight XCDs; giving each XCD a run of
 // consecutive units lets neighbours that read the same rows share its L2.
 __device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
@@ -183,6 +198,7 @@ struct DeltaChunkParams {
   void* y;
   char* img;           // [slots][H][kImgBytes]
   unsigned* words;     // workspace header
+  unsigned* amax;      // [rows][H]: bits of max |dy|, |dfinal| of a unit (backward)
   int64_t rows;        // sequences
   int64_t L, H, G, P;
   int64_t chunks;      // chunks per batch row (no cu)

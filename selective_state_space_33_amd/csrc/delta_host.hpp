@@ -35,6 +35,13 @@ inline bool delta_shape_supported(int64_t batch, int64_t L, int64_t heads, int64
   return batch * heads <= 0x7fffffffLL / ((headdim + 31) / 32);
 }
 
+// Chunks of 64 tokens: per batch row, or over packed sequences (delta_seq gives sequence s the slots from
+// cu[s] / 64 + s on).
+inline int64_t delta_slots(int64_t batch, int64_t L, int64_t nseq) {
+  return nseq > 0 ? L / 64 + nseq : batch * ((L + 63) / 64);
+}
+constexpr size_t kDeltaHeader = 256;
+
 inline ssm_status_t check_delta_args(const DeltaArgs& a, const void* y, const float* final_state) {
   if (!a.q || !a.k || !a.v || !a.delta || !a.A || !a.beta || !y) return SSM_ERR_INVALID_ARG;
   if (!delta_sizes_ok(a.batch, a.L, a.heads, a.headdim, a.ngroups, a.dstate)) return SSM_ERR_INVALID_ARG;

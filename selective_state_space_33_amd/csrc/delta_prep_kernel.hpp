@@ -49,7 +49,9 @@ template <int J> __device__ __forceinline__ void prep_column(float* sM, int lr, 
   }
 }
 
-template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkParams p) {
+// BWD: the image of the backward's walks instead (P without b, as a pair; the gates one by one).
+template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkParams p) {
+  constexpr int IMG = BWD ? kBwdImgBytes : kImgBytes, GATES = BWD ? kBwdGates : kImgGrow;
   constexpr int SB = DK + 8;  // bf16 row stride
   constexpr int ROWS = 2 * kDeltaC * SB * 2, MAT = kDeltaC * kPrepLd * 4;  // bytes
   __shared__ __attribute__((aligned(16))) char sMem[ROWS > MAT ? ROWS : MAT];
@@ -118,11 +120,20 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
       sChi[lane] = chi;
       sClo[lane] = static_cast<float>(cs - static_cast<double>(chi));
       sBeta[lane] = b;
-      float* img = reinterpret_cast<float*>(p.img + id * kImgBytes + kImgGrow);
+      float* img = reinterpret_cast<float*>(p.img + id * IMG + GATES);
       const float grow = __builtin_amdgcn_exp2f(chi * kLog2e);
       img[lane] = grow;
       img[64 + lane] = p.scale * grow;
-      img[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(end - cs) * kLog2e) * b;
+      const float left = __builtin_amdgcn_exp2f(static_cast<float>(end - cs) * kLog2e);
+      if constexpr (BWD) {
+        img[128 + lane] = left;
+        img[192 + lane] = b;
+        img[256 + lane] = chi;
+        img[320 + lane] = static_cast<float>(cs - static_cast<double>(chi));
+        if (c0 == 0 && lane == 0) p.amax[s * p.H + h] = 0u;  // before the walk that takes the maximum
+      } else {
+        img[128 + lane] = left * b;
+      }
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -172,14 +183,21 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * jt + 4 * lq + r;
-            acc[r] = j <= t ? p.scale * sBeta[j] * fade(t, j) * acc[r] : 0.0f;
+            acc[r] = j <= t ? p.scale * (BWD ? 1.0f : sBeta[j]) * fade(t, j) * acc[r] : 0.0f;
           }
         }
         half[u] = acc;
       }
-      // fp16: P meets R (fp16 too) in y alone, which is stored with 8 significant bits
-      *reinterpret_cast<f16x8_t*>(p.img + id * kImgBytes + kImgP + frag_of(tt, m2) * kFrag + lane * 16) =
-          pair_f16(half[0], half[1]);
+      char* out = p.img + id * IMG + kImgP + frag_of(tt, m2) * kFrag + lane * 16;
+      if constexpr (BWD) {
+        f16x8_t hi, lo;
+        split_f16(half[0], half[1], hi, lo);
+        *reinterpret_cast<f16x8_t*>(out) = hi;
+        *reinterpret_cast<f16x8_t*>(out + kBwdPlo - kImgP) = lo;
+      } else {
+        // fp16: P meets R (fp16 too) in y alone, which is stored with 8 significant bits
+        *reinterpret_cast<f16x8_t*>(out) = pair_f16(half[0], half[1]);
+      }
     }
   }
   __syncthreads();  // K and Q are read
@@ -230,7 +248,7 @@ template <int DK> __global__ void __launch_bounds__(256) delta_prep_kernel(Delta
     const f32x4_t x0 = block(2 * m), x1 = 2 * m + 1 <= t ? block(2 * m + 1) : zero;
     f16x8_t hi, lo;
     split_f16(x0, x1, hi, lo);
-    char* out = p.img + id * kImgBytes + f * kFrag + ln * 16;
+    char* out = p.img + id * IMG + f * kFrag + ln * 16;
     *reinterpret_cast<f16x8_t*>(out + kImgThi) = hi;
     *reinterpret_cast<f16x8_t*>(out + kImgTlo) = lo;
   }

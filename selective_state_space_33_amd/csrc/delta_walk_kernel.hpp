@@ -23,11 +23,6 @@
 
 namespace ssm {
 
-// A channel tile that the head does not have is addressed here: behind every resource (they are cut to this length,
-// and a chunk's offsets, 64 rows of at most 2^23 bytes, stay below half of it), so loads return zero and stores are
-// dropped.
-constexpr int kPastEnd = 0x40000000;
-
 // A tensor's next chunk: where it starts, and the length of the resource over it.  Only the last chunk's has to end
 // where the sequence does; past it there is nothing.
 struct DeltaStream {

@@ -76,15 +76,10 @@ bool delta_chunked(int64_t L, int64_t heads, int64_t headdim, int64_t dstate, in
   if (e) return atoi(e) != 0;
   return L / (nseq > 0 ? nseq : 1) > 16;
 }
-int64_t delta_slots(int64_t batch, int64_t L, int64_t nseq) {
-  return nseq > 0 ? L / kDeltaC + nseq : batch * ((L + kDeltaC - 1) / kDeltaC);
-}
-constexpr size_t kDeltaHeader = 256;
-
 template <int DK> hipError_t run_chunked(DeltaChunkParams& p, hipStream_t s) {
   const int64_t grid = p.slots * p.H;
   if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((delta_prep_kernel<DK, false>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t tiles = p.P / 16, units = p.rows * p.H;
@@ -145,7 +140,7 @@ extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* 
                        scale, dt};
   const ssm_status_t st = check_delta_args(a, y, final_state);
   if (st != SSM_OK) return st;
-  if (!delta_chunked(L, heads, headdim, dstate, nseq, dt) || !delta_aligned(y, 8)) {
+  if (!delta_chunked(L, heads, headdim, dstate, nseq, dt) || !delta_aligned(y, 8) || !delta_aligned(v, 8)) {
     DeltaStepParams p = step_params(a);
     p.hT = final_state;
     p.y = y;

@@ -36,6 +36,7 @@ EXPORTED = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_noalloc", "
             "ssm_state_update",
             "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_scan_trap_bwd_workspace_size", "ssm_scan_trap_bwd",
             "ssm_delta_fwd_workspace_size", "ssm_delta_fwd", "ssm_delta_update",
+            "ssm_delta_bwd_workspace_size", "ssm_delta_bwd",
             "ssm_gated_norm_fwd", "ssm_gated_norm_bwd_workspace_size", "ssm_gated_norm_bwd",
             "ssm_residual_norm_fwd", "ssm_residual_norm_bwd_workspace_size", "ssm_residual_norm_bwd",
             "ssm_workspace_status", "ssm_status_string")
@@ -99,6 +100,11 @@ def lib() -> ctypes.CDLL:
         L.ssm_delta_fwd_workspace_size.argtypes = [_i64] * 7 + [_int]
         L.ssm_delta_fwd.restype = _int
         L.ssm_delta_fwd.argtypes = ([_vp] * 7 + [_int, _int, _flt, _vp, _vp, _i64, _vp, _vp] + [_i64] * 6 +
+                                    [_int, _vp, _size, _vp])
+        L.ssm_delta_bwd_workspace_size.restype = _size
+        L.ssm_delta_bwd_workspace_size.argtypes = [_i64] * 7 + [_int]
+        L.ssm_delta_bwd.restype = _int
+        L.ssm_delta_bwd.argtypes = ([_vp] * 7 + [_int, _int, _flt] + [_vp] * 4 + [_i64] + [_vp] * 8 + [_i64] * 6 +
                                     [_int, _vp, _size, _vp])
         L.ssm_delta_update.restype = _int
         L.ssm_delta_update.argtypes = [_vp] * 8 + [_int, _int, _flt, _vp] + [_i64] * 5 + [_int, _vp]
@@ -546,6 +552,48 @@ def ssm_delta_fwd(q, k, v, delta, A, beta, delta_bias=None, softplus: bool = Tru
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_delta_fwd")
     return y, final_state
+
+
+def ssm_delta_bwd_workspace_size(batch: int, L: int, heads: int, headdim: int, ngroups: int, dstate: int, nseq: int,
+                                 dtype: torch.dtype) -> int:
+    return int(lib().ssm_delta_bwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq,
+                                                  _dtype_code(dtype)))
+
+
+def ssm_delta_bwd(q, k, v, delta, A, beta, dy, delta_bias=None, softplus: bool = True, sigmoid: bool = True,
+                  scale: Optional[float] = None, dfinal_state=None, initial_state=None,
+                  want_dinitial_state: bool = False, cu_seqlens=None, workspace=None, stream=None):
+    """Backward of ssm_delta_fwd: gradients of sum(y*dy) + sum(final_state*dfinal_state).
+
+    Inputs as ssm_delta_fwd (bfloat16) plus dy like v and dfinal_state like the states (or None).  Returns a dict of
+    dq, dk, dv, ddelta, dbeta (bfloat16), dA, ddelta_bias (None without a bias) and dinitial_state (when an initial
+    state is given or want_dinitial_state; float32).  With cu_seqlens, gradients of tokens of no sequence are zero."""
+    batch, L, heads, headdim, ngroups, dstate, nseq, rows = _delta_args(q, k, v, delta, A, beta, delta_bias,
+                                                                        initial_state, cu_seqlens)
+    dev, dt = v.device, v.dtype
+    code = _dtype_code(dt)
+    _check(dy, "dy", dt, (batch, L, heads, headdim), dev)
+    _check(dfinal_state, "dfinal_state", torch.float32, (rows, heads, headdim, dstate), dev)
+    s = _resolve(dev, stream)
+    with torch.cuda.stream(s):
+        # tokens of no sequence are not written by the call
+        new = torch.empty_like if cu_seqlens is None else torch.zeros_like
+        g = dict(dq=new(q), dk=new(k), dv=new(v), ddelta=new(delta), dA=torch.empty_like(A), dbeta=new(beta),
+                 ddelta_bias=None if delta_bias is None else torch.empty_like(delta_bias),
+                 dinitial_state=(torch.empty((rows, heads, headdim, dstate), dtype=torch.float32, device=dev)
+                                 if (initial_state is not None or want_dinitial_state) else None))
+        need = ssm_delta_bwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq, dt)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = lib().ssm_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta), _ptr(delta_bias),
+                             1 if softplus else 0, 1 if sigmoid else 0, dstate ** -0.5 if scale is None else scale,
+                             _ptr(dy), _ptr(dfinal_state), _ptr(initial_state), _ptr(cu_seqlens), nseq, _ptr(g["dq"]),
+                             _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddelta"]), _ptr(g["dA"]), _ptr(g["dbeta"]),
+                             _ptr(g["ddelta_bias"]), _ptr(g["dinitial_state"]), batch, L, heads, headdim, ngroups,
+                             dstate, code, _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
+    if rc != SSM_OK:
+        raise SSMError(rc, "ssm_delta_bwd")
+    return g
 
 
 def ssm_delta_update(state, q, k, v, delta, A, beta, delta_bias=None, softplus: bool = True, sigmoid: bool = True,

@@ -142,3 +142,26 @@ def test_binding_checks_tensors():
     with pytest.raises(ValueError, match="k has shape|q has shape"):
         ops.ssm_delta_fwd(torch.zeros(1, 3, 2, 32), torch.zeros(1, 4, 2, 32), torch.zeros(1, 4, 4, 16),
                           torch.zeros(1, 4, 4), torch.zeros(4), torch.zeros(1, 4, 4))
+
+
+@pytest.mark.parametrize("kw,expect", SHARED + [
+    (dict(dy=None), INVALID), (dict(dq=None), INVALID), (dict(dk=None), INVALID), (dict(dv=None), INVALID),
+    (dict(dd=None), INVALID), (dict(dA=None), INVALID), (dict(db=None), INVALID), (dict(L=0), INVALID),
+    (dict(v=0x3008), INVALID), (dict(dy=0x8008), INVALID), (dict(dv=0xb008), INVALID), (dict(dq=0x9001), INVALID),
+    (dict(dA=0xd002), INVALID), (dict(dfs=0xe008), INVALID), (dict(dh0=0xf008), INVALID),
+    (dict(dt=F32), UNSUPPORTED), (dict(N=192), UNSUPPORTED), (dict(P=40), UNSUPPORTED),
+    (dict(H=1 << 16, P=128), UNSUPPORTED), (dict(cu=0x9000, nseq=2, batch=2), INVALID),
+    (dict(ws=None), INVALID), (dict(ws=0x100010), INVALID), (dict(wsb=4096), INVALID),
+])
+def test_delta_bwd_refuses(kw, expect):
+    a = dict(q=0x1000, k=0x2000, v=0x3000, delta=0x4000, A=0x5000, beta=0x6000, bias=None, dy=0x8000, dfs=None,
+             h0=None, cu=None, nseq=0, dq=0x9000, dk=0xa000, dv=0xb000, dd=0xc000, dA=0xd000, db=0xe000, dbias=None,
+             dh0=None, y=0, batch=1, L=100, H=4, P=64, G=2, N=64, dt=BF16, ws=0x100000, wsb=1 << 40)
+    a.update(kw)
+    if "y" in kw:       # the shared list's misaligned y is this call's dy
+        a["dy"] = kw["y"]
+    rc = ops.lib().ssm_delta_bwd(a["q"], a["k"], a["v"], a["delta"], a["A"], a["beta"], a["bias"], 1, 1, 1.0, a["dy"],
+                                 a["dfs"], a["h0"], a["cu"], a["nseq"], a["dq"], a["dk"], a["dv"], a["dd"], a["dA"],
+                                 a["db"], a["dbias"], a["dh0"], a["batch"], a["L"], a["H"], a["P"], a["G"], a["N"],
+                                 a["dt"], a["ws"], a["wsb"], None)
+    assert rc == expect
