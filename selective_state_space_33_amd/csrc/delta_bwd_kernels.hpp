@@ -29,7 +29,7 @@
 // Precision.  What goes from chunk to chunk, dV and every term of dla is a pair
 // of fp16 (22 bits) in fp32 accumulators.  dY and what is linear in it may have
 // any magnitude, so a unit's dY and final gradient are scaled by the power of
-// two that brings their largest element to [1, 2) and the results scaled back,
+// two that brings their largest element to [16, 32) and the results scaled back,
 // both exactly; dq, dk and db, stored as bf16, take their operands as one fp16.
 #pragma once
 
@@ -62,12 +62,13 @@ struct DeltaBwdParams {
   int64_t tiles;        // P / 16
 };
 
-// The scale of a unit's gradients: 2^-e for a largest magnitude in [2^e, 2^(e+1)), within what fp32 holds on both
-// sides; 1 where there is none, or none that is finite.
+// The scale of a unit's gradients: it brings their largest magnitude to [16, 32), within what fp32 holds on both
+// sides; 1 where there is none, or none that is finite.  (What is summed from them stays thousands of times below the
+// largest fp16, and the lo part of a pair, whose last place is 2^-24, keeps its bits down to 2^-3.)
 __device__ __forceinline__ float grad_scale(unsigned amax_bits) {
   const int e = static_cast<int>(amax_bits >> 23) - 127;
   if (amax_bits == 0u || e > 127) return 1.0f;
-  const int s = e < -100 ? 100 : (e > 100 ? -100 : -e);
+  const int s = e < -96 ? 100 : (e > 104 ? -100 : 4 - e);
   return __uint_as_float(static_cast<unsigned>(s + 127) << 23);
 }
 
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(64 * W) delta_bwd_walk_kernel(DeltaBwdParams b
           const int e = 4 * (t & 1) + r;
           l[r] = x[t][r] * (static_cast<float>(r0[t >> 1][e]) + static_cast<float>(r0[2 + (t >> 1)][e])) * beta[r];
         }
+        x[t] *= kBwdPScale;
         l = sum_lanes16(l);
         if (mine && lr == 0) *reinterpret_cast<f32x4_t*>(&bp.lterm[mytile * kDeltaC + 16 * t + 4 * lq]) = l * inv;
       }
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(64 * W) delta_bwd_walk_kernel(DeltaBwdParams b
           x[t] = mfma_f16(bwd_col_frag(sImg, 12, t, m, lr, lq), Df[m], x[t]);
           x[t] = mfma_f16(bwd_col_frag(sImg, 18, t, m, lr, lq), Df[m], x[t]);
         }
-        x[t] *= bwd_gate(sImg, kBwdBeta, t, lq);
+        x[t] *= bwd_gate(sImg, kBwdBeta, t, lq) * (1.0f / kBwdPScale);
       }
       // dV = T^T diag(b) Y0, kept as a pair; its transpose (rows of channels, from the hi parts) to store as bf16
       f16x8_t Zh[2], Zl[2];
@@ -503,7 +505,7 @@ template <int LD> __device__ __forceinline__ f16x8_t tok_frag(const uint16_t* ba
   return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
 }
 
-template <int DK> __global__ void __launch_bounds__(256) delta_grad_kernel(DeltaBwdParams bp) {
+template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaBwdParams bp) {
   const DeltaChunkParams& p = bp.c;
   constexpr int KT = DK / 32, DT = DK / 16, CL = kColLd<DK>;
   __shared__ DeltaGradLds<DK> lds;
@@ -550,7 +552,8 @@ template <int DK> __global__ void __launch_bounds__(256) delta_grad_kernel(Delta
     }
   }
   const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  f32x4_t dq[DT], dk[DT];
+  f32x4_t dq[DT], dk[DT];  // in the scale of the head at work
+  float unscale = 1.0f;
 #pragma unroll
   for (int d = 0; d < DT; ++d) dq[d] = dk[d] = zero;
   const int nb = static_cast<int>((bp.tiles + 1) / 2);  // blocks of 32 channels
@@ -586,11 +589,17 @@ template <int DK> __global__ void __launch_bounds__(256) delta_grad_kernel(Delta
                                                  ra, some ? (2 * b + u) * (KT * kFrag) + f * 16 : kPastEnd, 0, 0));
       }
     };
-    f32x4_t d1t[4], d1[4], d2t[4], d2[4], q0[DT], ws[DT], rd[DT];
+    // dy . r and dv . r.  Of the tiles of this wavefront's tokens (as t, lane by lane) with those before them: a1, a2 at
+    // their tile; with those behind them (this wavefront's as j): a1, a2 at theirs; its tile with itself both ways.
+    f32x4_t a1[4], a2[4], b1 = zero, b2 = zero, aw[DT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) d1t[t] = d1[t] = d2t[t] = d2[t] = zero;
+    for (int t = 0; t < 4; ++t) a1[t] = a2[t] = zero;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) q0[d] = ws[d] = rd[d] = zero;
+    for (int d = 0; d < DT; ++d) {
+      aw[d] = zero;
+      dq[d] *= sc * unscale, dk[d] *= sc * unscale;  // from the last head's scale to this one's
+    }
+    unscale = inv;
     load(0);
     for (int b = 0; b < nb; ++b) {
       __syncthreads();  // the last block (or head) is read
@@ -641,58 +650,70 @@ template <int DK> __global__ void __launch_bounds__(256) delta_grad_kernel(Delta
         // as pairs where the terms go into dla, one fp16 each in the transposes (for dk)
         if (t <= w) {
           const f16x8_t rt = tok_frag<kGradTok>(lds.r, t, lr, lq), rtl = tok_frag<kGradTokLo>(lds.rl, t, lr, lq);
-          d1t[t] = mfma_f16(rtl, yw, d1t[t]);
-          d2t[t] = mfma_f16(rtl, vw, d2t[t]);
-          d1t[t] = mfma_f16(rt, yw, d1t[t]);
-          d2t[t] = mfma_f16(rt, vwl, d2t[t]);
-          d2t[t] = mfma_f16(rt, vw, d2t[t]);
-        }
-        if (t >= w) {
-          d1[t] = mfma_f16(yrows(t), rw, d1[t]);
-          d2[t] = mfma_f16(tok_frag<kGradTok>(lds.v, t, lr, lq), rw, d2[t]);
+          a1[t] = mfma_f16(rtl, yw, a1[t]);
+          a2[t] = mfma_f16(rtl, vw, a2[t]);
+          a1[t] = mfma_f16(rt, yw, a1[t]);
+          a2[t] = mfma_f16(rt, vwl, a2[t]);
+          a2[t] = mfma_f16(rt, vw, a2[t]);
+        } else {
+          a1[t] = mfma_f16(yrows(t), rw, a1[t]);
+          a2[t] = mfma_f16(tok_frag<kGradTok>(lds.v, t, lr, lq), rw, a2[t]);
         }
       }
+      b1 = mfma_f16(yw, rw, b1);
+      b2 = mfma_f16(vw, rw, b2);
+      // the rows' gates go into the operands (another rounding to fp16), so the products add to dq and dk themselves
+      const f16x8_t yo = yw * static_cast<_Float16>(lds.g[1][16 * w + lr]);
+      const f16x8_t vg = vw * static_cast<_Float16>(-lds.g[0][16 * w + lr]);
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         const f16x8_t sf = lds_col_frag<DK>(lds.s, 0, d, lr, lq), af = lds_col_frag<DK>(lds.a, 0, d, lr, lq);
-        q0[d] = mfma_f16(yw, sf, q0[d]);
-        rd[d] = mfma_f16(vw, sf, rd[d]);
-        ws[d] = mfma_f16(rw, af, ws[d]);
+        dq[d] = mfma_f16(yo, sf, dq[d]);
+        dk[d] = mfma_f16(vg, sf, dk[d]);
+        aw[d] = mfma_f16(rw, af, aw[d]);
       }
     }
     __syncthreads();  // the blocks are read: their place takes the pair terms
-    // ---- the chunk's own products.  A lane's elements: of d1t, d2t (j = 16 t + 4 lq + r, token 16 w + lr); of d1, d2
-    // (t = 16 t + 4 lq + r, j = 16 w + lr)
-    const float* grow = lds.g[0];
-    const float* outg = lds.g[1];
+    // ---- the chunk's own products.  A lane's elements: before and on this wavefront's tile, (j = 16 t + 4 lq + r,
+    // token 16 w + lr); behind it, (token 16 t + 4 lq + r, j = 16 w + lr), and so b1, b2
     const float* left = lds.g[2];
     const float* beta = lds.g[3];
     auto fade = [&](int t, int j) {
       return __builtin_amdgcn_exp2f(((lds.g[4][t] - lds.g[4][j]) + (lds.g[5][t] - lds.g[5][j])) * kLog2e);
     };
     const int me = 16 * w + lr;
-    // the fades where they matter: past the diagonal the exponent may be anything
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      // q_t . k_j and k_t . k_j of the pair terms (the operands are exact)
-      f32x4_t qk = zero, kk = zero;
       if (t <= w) {
+        // q_t . k_j and k_t . k_j of the pair terms (the operands are exact)
+        f32x4_t qk = zero, kk = zero;
 #pragma unroll
         for (int e = 0; e < KT; ++e) {
           const f16x8_t kj = plain_row_frag<CL>(sK, 16 * t + lr, e, lq);
           qk = mfma_f16(kj, plain_row_frag<CL>(sQ, me, e, lq), qk);
           kk = mfma_f16(kj, plain_row_frag<CL>(sK, me, e, lq), kk);
         }
-      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int o = 16 * t + 4 * lq + r;
-        const float f1 = o <= me ? fade(me, o) * beta[o] : 0.0f, f2 = o >= me ? fade(o, me) : 0.0f;
-        d1t[t][r] *= p.scale * f1;
-        d2t[t][r] = o < me ? -f1 * d2t[t][r] : 0.0f;
-        d1[t][r] *= p.scale * f2;
-        d2[t][r] = o > me ? -f2 * d2[t][r] : 0.0f;
-        if (t <= w) lds.c[me * kGradC + o] = o < me ? d1t[t][r] * qk[r] + d2t[t][r] * kk[r] : 0.0f;
+        for (int r = 0; r < 4; ++r) {
+          // the fades where they matter: past the diagonal the exponent may be anything
+          const int o = 16 * t + 4 * lq + r;
+          const float f = o <= me ? fade(me, o) * beta[o] : 0.0f;
+          a1[t][r] *= p.scale * f;
+          a2[t][r] = o < me ? -f * a2[t][r] : 0.0f;
+          lds.c[me * kGradC + o] = o < me ? a1[t][r] * qk[r] + a2[t][r] * kk[r] : 0.0f;
+          if (t == w) {
+            const float f2 = o >= me ? fade(o, me) : 0.0f;
+            b1[r] *= p.scale * f2;
+            b2[r] = o > me ? -f2 * b2[r] : 0.0f;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float f = fade(16 * t + 4 * lq + r, me);
+          a1[t][r] *= p.scale * f;
+          a2[t][r] *= -f;
+        }
       }
     }
     __syncthreads();
@@ -707,42 +728,42 @@ template <int DK> __global__ void __launch_bounds__(256) delta_grad_kernel(Delta
       if (part == 0) lds.e[t] = e;
     }
     __syncthreads();
-    const f32x4_t outw = *reinterpret_cast<const f32x4_t*>(&outg[16 * w + 4 * lq]);
     const f32x4_t leftw = *reinterpret_cast<const f32x4_t*>(&left[16 * w + 4 * lq]);
     const f32x4_t betaw = *reinterpret_cast<const f32x4_t*>(&beta[16 * w + 4 * lq]);
-    const f32x4_t groww = *reinterpret_cast<const f32x4_t*>(&grow[16 * w + 4 * lq]);
-    f16x8_t a1[2], b1[2], c1[2], e1[2];
+    // operands of the halves m of the tokens: this wavefront's as t with what is before (P, -N), as j with what follows
+    f16x8_t pt[2], nt2[2], pj[2], nj[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      a1[m] = pair_f16(d1t[2 * m], d1t[2 * m + 1]);
-      b1[m] = pair_f16(d2t[2 * m], d2t[2 * m + 1]);
-      c1[m] = pair_f16(d1[2 * m], d1[2 * m + 1]);
-      e1[m] = pair_f16(d2[2 * m], d2[2 * m + 1]);
+      auto before = [&](const f32x4_t& v, int t) { return t <= w ? v : zero; };
+      auto behind = [&](const f32x4_t& v, const f32x4_t& own, int t) { return t > w ? v : (t == w ? own : zero); };
+      pt[m] = pair_f16(before(a1[2 * m], 2 * m), before(a1[2 * m + 1], 2 * m + 1));
+      nt2[m] = pair_f16(before(a2[2 * m], 2 * m), before(a2[2 * m + 1], 2 * m + 1));
+      pj[m] = pair_f16(behind(a1[2 * m], b1, 2 * m), behind(a1[2 * m + 1], b1, 2 * m + 1));
+      nj[m] = pair_f16(behind(a2[2 * m], b2, 2 * m), behind(a2[2 * m + 1], b2, 2 * m + 1));
     }
     float db[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      f32x4_t aq = q0[d] * outw, aw = ws[d] * leftw, ak = rd[d] * -groww;
+      aw[d] *= leftw;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const f16x8_t kc = lds_col_frag<DK>(sK, 32 * m, d, lr, lq);
         if (2 * m <= w) {  // tokens up to this wavefront's
-          aq = mfma_f16(a1[m], kc, aq);
-          ak = mfma_f16(b1[m], kc, ak);
+          dq[d] = mfma_f16(pt[m], kc, dq[d]);
+          dk[d] = mfma_f16(nt2[m], kc, dk[d]);
         }
         if (2 * m + 1 >= w) {  // and from it on
-          aw = mfma_f16(c1[m], lds_col_frag<DK>(sQ, 32 * m, d, lr, lq), aw);
-          aw = mfma_f16(e1[m], kc, aw);
+          aw[d] = mfma_f16(pj[m], lds_col_frag<DK>(sQ, 32 * m, d, lr, lq), aw[d]);
+          aw[d] = mfma_f16(nj[m], kc, aw[d]);
         }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float kv = static_cast<float>(
             __builtin_bit_cast(_Float16, sK[(16 * w + 4 * lq + r) * CL + 16 * d + lr]));
-        db[r] = __builtin_fmaf(kv, aw[r], db[r]);
+        db[r] = __builtin_fmaf(kv, aw[d][r], db[r]);
       }
-      dq[d] += aq * inv;
-      dk[d] += (aw * betaw + ak) * inv;
+      dk[d] += aw[d] * betaw;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -795,8 +816,8 @@ template <int DK> __global__ void __launch_bounds__(256) delta_grad_kernel(Delta
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int at = static_cast<int>(((16 * w + 4 * lq + r) * krow + 16 * d + lr) * 2);
-      __builtin_amdgcn_raw_buffer_store_b16(to_bf16(dq[d][r]), oq, at, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b16(to_bf16(dk[d][r]), ok, at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b16(to_bf16(dq[d][r] * unscale), oq, at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b16(to_bf16(dk[d][r] * unscale), ok, at, 0, 0);
     }
 }
 

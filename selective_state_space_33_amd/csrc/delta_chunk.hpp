@@ -50,6 +50,7 @@ constexpr int kImgOut = kImgGrow + 256;      // scale e^{cs_t}
 constexpr int kImgLeft = kImgGrow + 512;     // e^{cs_C - cs_t} b_t (0 behind the sequence's end)
 constexpr int kImgBytes = kImgGrow + 768;
 // The backward's image: the same fragments of T, then P without b as a pair, and the gates.
+constexpr float kBwdPScale = 16.0f;          // P is kept 16 times as large, away from the last places of fp16
 constexpr int kBwdPlo = 18 * kFrag;
 constexpr int kBwdGates = 24 * kFrag;
 constexpr int kBwdGrow = kBwdGates;          // e^{cs_t}

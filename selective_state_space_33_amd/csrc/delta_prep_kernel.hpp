@@ -183,7 +183,7 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * jt + 4 * lq + r;
-            acc[r] = j <= t ? p.scale * (BWD ? 1.0f : sBeta[j]) * fade(t, j) * acc[r] : 0.0f;
+            acc[r] = j <= t ? p.scale * (BWD ? kBwdPScale : sBeta[j]) * fade(t, j) * acc[r] : 0.0f;
           }
         }
         half[u] = acc;
