@@ -559,6 +559,11 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
   const int nb = static_cast<int>((bp.tiles + 1) / 2);  // blocks of 32 channels
   for (int64_t hh = 0; hh < rep; ++hh) {
     const int64_t h = g * rep + hh, cell = slot * p.H + h;
+    // What a lane derives from its place is derived anew for every head: carried over the loop, the addresses and the
+    // masks of the triangles took a hundred registers more than there are.
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, lr = lane & 15, lq = lane >> 4;
     const float sc = grad_scale(p.amax[s * p.H + h]), inv = 1.0f / sc;
     const int tbytes = static_cast<int>(bp.tiles * kFrag);
     const rsrc_t rr = make_rsrc(bp.r + cell * bp.tiles * (4 * kFrag), 4 * tbytes);
@@ -659,7 +664,9 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
           a1[t] = mfma_f16(yrows(t), rw, a1[t]);
           a2[t] = mfma_f16(tok_frag<kGradTok>(lds.v, t, lr, lq), rw, a2[t]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_sched_barrier(0);
       b1 = mfma_f16(yw, rw, b1);
       b2 = mfma_f16(vw, rw, b2);
       // the rows' gates go into the operands (another rounding to fp16), so the products add to dq and dk themselves
@@ -671,6 +678,7 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
         dq[d] = mfma_f16(yo, sf, dq[d]);
         dk[d] = mfma_f16(vg, sf, dk[d]);
         aw[d] = mfma_f16(rw, af, aw[d]);
+        if (d & 1) __builtin_amdgcn_sched_barrier(0);  // fragments of all d at once would not fit the registers
       }
     }
     __syncthreads();  // the blocks are read: their place takes the pair terms
@@ -678,10 +686,8 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
     // token 16 w + lr); behind it, (token 16 t + 4 lq + r, j = 16 w + lr), and so b1, b2
     const float* left = lds.g[2];
     const float* beta = lds.g[3];
-    auto fade = [&](int t, int j) {
-      return __builtin_amdgcn_exp2f(((lds.g[4][t] - lds.g[4][j]) + (lds.g[5][t] - lds.g[5][j])) * kLog2e);
-    };
     const int me = 16 * w + lr;
+    const float hme = lds.g[4][me], lme = lds.g[5][me];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (t <= w) {
@@ -693,24 +699,36 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
           qk = mfma_f16(kj, plain_row_frag<CL>(sQ, me, e, lq), qk);
           kk = mfma_f16(kj, plain_row_frag<CL>(sK, me, e, lq), kk);
         }
+        const f32x4_t bj = *reinterpret_cast<const f32x4_t*>(&beta[16 * t + 4 * lq]);
+        const f32x4_t hj = *reinterpret_cast<const f32x4_t*>(&lds.g[4][16 * t + 4 * lq]);
+        const f32x4_t lj = *reinterpret_cast<const f32x4_t*>(&lds.g[5][16 * t + 4 * lq]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          // the fades where they matter: past the diagonal the exponent may be anything
           const int o = 16 * t + 4 * lq + r;
-          const float f = o <= me ? fade(me, o) * beta[o] : 0.0f;
-          a1[t][r] *= p.scale * f;
-          a2[t][r] = o < me ? -f * a2[t][r] : 0.0f;
-          lds.c[me * kGradC + o] = o < me ? a1[t][r] * qk[r] + a2[t][r] * kk[r] : 0.0f;
-          if (t == w) {
-            const float f2 = o >= me ? fade(o, me) : 0.0f;
+          // log of the fade from j = o to this token; past the diagonal (in the own tile) it may be anything
+          const float x = ((hme - hj[r]) + (lme - lj[r])) * kLog2e;
+          if (t < w) {
+            const float f = __builtin_amdgcn_exp2f(x) * bj[r];
+            a1[t][r] *= p.scale * f;
+            a2[t][r] *= -f;
+            lds.c[me * kGradC + o] = a1[t][r] * qk[r] + a2[t][r] * kk[r];
+          } else {
+            const int rel = 4 * lq + r - lr;
+            const float f = rel <= 0 ? __builtin_amdgcn_exp2f(x) * bj[r] : 0.0f;
+            const float f2 = rel >= 0 ? __builtin_amdgcn_exp2f(-x) : 0.0f;
+            a1[t][r] *= p.scale * f;
+            a2[t][r] = rel < 0 ? -f * a2[t][r] : 0.0f;
+            lds.c[me * kGradC + o] = rel < 0 ? a1[t][r] * qk[r] + a2[t][r] * kk[r] : 0.0f;
             b1[r] *= p.scale * f2;
-            b2[r] = o > me ? -f2 * b2[r] : 0.0f;
+            b2[r] = rel > 0 ? -f2 * b2[r] : 0.0f;
           }
         }
       } else {
+        const f32x4_t ht = *reinterpret_cast<const f32x4_t*>(&lds.g[4][16 * t + 4 * lq]);
+        const f32x4_t lt = *reinterpret_cast<const f32x4_t*>(&lds.g[5][16 * t + 4 * lq]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float f = fade(16 * t + 4 * lq + r, me);
+          const float f = __builtin_amdgcn_exp2f(((ht[r] - hme) + (lt[r] - lme)) * kLog2e);
           a1[t][r] *= p.scale * f;
           a2[t][r] *= -f;
         }
@@ -764,6 +782,7 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
         db[r] = __builtin_fmaf(kv, aw[d][r], db[r]);
       }
       dk[d] += aw[d] * betaw;
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
