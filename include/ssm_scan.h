@@ -446,8 +446,8 @@ size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int
  *   in ssm_delta_fwd: rows of no sequence are left as they were, and an empty
  *   sequence hands dfinal_state to dinitial_state unchanged.
  *   dt = BF16, dstate 32, 64, 96 or 128, headdim a multiple of 16, heads *
- *   headdim and heads * dstate up to 2^22; else UNSUPPORTED.  q, k, v, dy, dv
- *   and the states 16-byte aligned, everything else to its element.  Only
+ *   headdim and heads * dstate up to 2^22; else UNSUPPORTED.  q, k, v, dy, dq,
+ *   dk, dv and the states 16-byte aligned, everything else to its element.  Only
  *   dfinal_state and dinitial_state may be the same buffer; no other output
  *   may alias anything.  q, k, v and the states must stay below 65504 in
  *   magnitude (ssm_delta_fwd); dy and dfinal_state may have any magnitude:

@@ -491,9 +491,11 @@ template <int DK> struct DeltaGradLds {
           vl[32 * kGradTokLo], y[kDeltaC * kGradLd], s[32 * CL], a[32 * CL];
     };
     struct {
-      float c[kDeltaC * kGradC];  // once the blocks are read: the pair terms, and rows less columns of them
-      double e[kDeltaC];
+      // once the blocks are read: the pair terms, rows less columns of them, and each wavefront's sums over its tiles
+      float c[kDeltaC * kGradC];
+      double e[kDeltaC], og[4][kDeltaC], l[4][kDeltaC], edge[4];
     };
+    uint16_t out[2][kDeltaC * CL];  // at the end: dq and dk on their way to whole rows
   };
   __attribute__((aligned(16))) float g[6][kDeltaC];  // the image's gates
 };
@@ -537,18 +539,17 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
   const int64_t tok = sq.tok + c0;
   const int64_t krow = p.G * DK, rowe = p.H * p.P;
   const int64_t kb = tok * krow + g * DK, kbytes = ((nt - 1) * krow + DK) * 2;
+  constexpr int KPER = kDeltaC * DK / 8 / 256;
+  u32x4_t g_k[KPER], g_q[KPER];
   {
     const rsrc_t rk = make_rsrc(static_cast<const uint16_t*>(p.k) + kb, kbytes);
     const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(p.q) + kb, kbytes);
-    constexpr int PER = kDeltaC * DK / 8 / 256;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int i = 0; i < KPER; ++i) {
       const int e = tid + 256 * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
       const int off = static_cast<int>((row * krow + cc) * 2);
-      *reinterpret_cast<u32x4_t*>(&sK[row * CL + cc]) =
-          bf16x8_as_f16(__builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0)));
-      *reinterpret_cast<u32x4_t*>(&sQ[row * CL + cc]) =
-          bf16x8_as_f16(__builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0)));
+      g_k[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0));
+      g_q[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
     }
   }
   const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -606,11 +607,27 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
     }
     unscale = inv;
     load(0);
+    f32x4_t g_g = zero;  // the gates, a lane four
+    if (tid < 6 * 16) g_g = *reinterpret_cast<const f32x4_t*>(p.img + cell * kBwdImgBytes + kBwdGates + tid * 16);
+    if (hh == 0) {  // K and Q, loaded ahead of all of this
+#pragma unroll
+      for (int i = 0; i < KPER; ++i) {
+        const int e = tid + 256 * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
+        *reinterpret_cast<u32x4_t*>(&sK[row * CL + cc]) = bf16x8_as_f16(g_k[i]);
+        *reinterpret_cast<u32x4_t*>(&sQ[row * CL + cc]) = bf16x8_as_f16(g_q[i]);
+      }
+    }
+    // dla's terms of each token (a lane) over every fourth tile
+    double og = 0.0, lt = 0.0, edge = 0.0;
+    for (int64_t t = w; t < bp.tiles; t += 4) {
+      const int64_t at = (cell * bp.tiles + t) * kDeltaC + lane;
+      og += static_cast<double>(bp.oterm[at]) - static_cast<double>(bp.gterm[at]);
+      lt += bp.lterm[at];
+      edge += bp.edge[cell * bp.tiles + t];
+    }
     for (int b = 0; b < nb; ++b) {
       __syncthreads();  // the last block (or head) is read
-      if (b == 0 && tid < 6 * 16)
-        *reinterpret_cast<f32x4_t*>(&lds.g[0][0] + tid * 4) =
-            *reinterpret_cast<const f32x4_t*>(p.img + cell * kBwdImgBytes + kBwdGates + tid * 16);
+      if (b == 0 && tid < 6 * 16) *reinterpret_cast<f32x4_t*>(&lds.g[0][0] + tid * 4) = g_g;
       {
         const int row = tid >> 2, cc = 8 * (tid & 3);
         u32x4_t y8;
@@ -739,11 +756,18 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
       // rows less columns of the pair terms, four threads a token
       const int t = tid >> 2, part = tid & 3;
       double e = 0.0;
-      for (int o = part; o < t; o += 4) e += lds.c[t * kGradC + o];
-      for (int o = t + 1 + part; o < kDeltaC; o += 4) e -= lds.c[o * kGradC + t];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int o = part + 4 * i;
+        const float v = lds.c[o < t ? t * kGradC + o : o * kGradC + t];
+        e += o < t ? static_cast<double>(v) : (o > t ? -static_cast<double>(v) : 0.0);
+      }
       e += __shfl_xor(e, 1, 64);
       e += __shfl_xor(e, 2, 64);
       if (part == 0) lds.e[t] = e;
+      lds.og[w][lane] = og;
+      lds.l[w][lane] = lt;
+      if (lane == 0) lds.edge[w] = edge;
     }
     __syncthreads();
     const f32x4_t leftw = *reinterpret_cast<const f32x4_t*>(&left[16 * w + 4 * lq]);
@@ -796,13 +820,9 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
     }
     if (w == 0) {
       // ---- the fades' gradient: sums over the tokens behind each, and over those before it, in fp64
-      double la = lds.e[lane] * inv, lt = 0.0, e = 0.0;
-      for (int64_t t = 0; t < bp.tiles; ++t) {
-        const int64_t at = (cell * bp.tiles + t) * kDeltaC + lane;
-        la += static_cast<double>(bp.oterm[at]) - static_cast<double>(bp.gterm[at]);
-        lt += bp.lterm[at];
-        e += bp.edge[cell * bp.tiles + t];
-      }
+      double la = lds.e[lane] * inv + ((lds.og[0][lane] + lds.og[1][lane]) + (lds.og[2][lane] + lds.og[3][lane]));
+      double e = (lds.edge[0] + lds.edge[1]) + (lds.edge[2] + lds.edge[3]);
+      lt = (lds.l[0][lane] + lds.l[1][lane]) + (lds.l[2][lane] + lds.l[3][lane]);
       const double own = lt;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -828,16 +848,26 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
       }
     }
   }
-  const rsrc_t oq = make_rsrc(static_cast<uint16_t*>(bp.dq) + kb, kbytes);
-  const rsrc_t ok = make_rsrc(static_cast<uint16_t*>(bp.dk) + kb, kbytes);
+  // dq and dk through LDS, so that they leave in whole 16-byte pieces
+  __syncthreads();
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int at = static_cast<int>(((16 * w + 4 * lq + r) * krow + 16 * d + lr) * 2);
-      __builtin_amdgcn_raw_buffer_store_b16(to_bf16(dq[d][r] * unscale), oq, at, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b16(to_bf16(dk[d][r] * unscale), ok, at, 0, 0);
+      const int at = (16 * w + 4 * lq + r) * CL + 16 * d + lr;
+      lds.out[0][at] = to_bf16(dq[d][r] * unscale);
+      lds.out[1][at] = to_bf16(dk[d][r] * unscale);
     }
+  __syncthreads();
+  const rsrc_t oq = make_rsrc(static_cast<uint16_t*>(bp.dq) + kb, kbytes);
+  const rsrc_t ok = make_rsrc(static_cast<uint16_t*>(bp.dk) + kb, kbytes);
+#pragma unroll
+  for (int i = 0; i < KPER; ++i) {
+    const int e = tid + 256 * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
+    const int off = static_cast<int>((row * krow + cc) * 2);
+    __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4_t*>(&lds.out[0][row * CL + cc]), oq, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4_t*>(&lds.out[1][row * CL + cc]), ok, off, 0, 0);
+  }
 }
 
 // dA and dbias of a head: the chunks' parts, summed in a fixed order.

@@ -94,11 +94,11 @@ extern "C" ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* 
   const ssm_status_t st = check_delta_args(a, dy, dinitial_state);
   if (st != SSM_OK) return st;
   if (!dq || !dk || !dv || !ddelta || !dA || !dbeta) return SSM_ERR_INVALID_ARG;
-  // v, dy and dv pass in 8- and 16-byte pieces
-  if (!delta_aligned(v, 16) || !delta_aligned(dy, 16) || !delta_aligned(dv, 16)) return SSM_ERR_INVALID_ARG;
-  const void* halves[] = {dq, dk, ddelta, dbeta};
-  for (const void* o : halves)
-    if (!delta_aligned(o, 2)) return SSM_ERR_INVALID_ARG;
+  // v, dy and the gradients of q, k and v pass in 8- and 16-byte pieces
+  const void* wide[] = {v, dy, dq, dk, dv};
+  for (const void* o : wide)
+    if (!delta_aligned(o, 16)) return SSM_ERR_INVALID_ARG;
+  if (!delta_aligned(ddelta, 2) || !delta_aligned(dbeta, 2)) return SSM_ERR_INVALID_ARG;
   if (!delta_aligned(dA, 4) || (ddelta_bias && !delta_aligned(ddelta_bias, 4)) ||
       (dfinal_state && !delta_aligned(dfinal_state, 16)))
     return SSM_ERR_INVALID_ARG;
