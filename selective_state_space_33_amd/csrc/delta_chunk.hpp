@@ -208,4 +208,30 @@ struct DeltaChunkParams {
   float scale;
 };
 
+// Of the backward (delta_bwd_kernels.hpp).
+struct DeltaBwdParams {
+  DeltaChunkParams c;
+  const void* dy;       // [tokens][H][P] bf16
+  const float* dfinal;  // [rows][H][P][N] (nullable)
+  void* dq;             // [tokens][G][N] bf16
+  void* dk;
+  void* dv;             // [tokens][H][P] bf16
+  void* ddelta;         // [tokens][H] bf16
+  void* dbeta;
+  float* dh0;           // [rows][H][P][N] (nullable)
+  // kept as operand fragments, [slots][H][tiles][...][kFrag]: S0 [2][KT] (hi, lo), dS [KT] (scaled), R and dV (scaled)
+  // [2][2] (hi, lo; two halves of the tokens, channel by channel)
+  char* state;
+  char* adj;
+  char* r;
+  char* dvh;
+  // parts of dla over a tile's 16 channels, [slots][H][tiles][64]: the terms of S0 and Q, of S0 and K, of dS and K
+  float* oterm;
+  float* gterm;
+  float* lterm;
+  float* edge;          // [slots][H][tiles]: e^{cs_C} <dS, S0>
+  float* part;          // [slots][H][2]: parts of dA and dbias
+  int64_t tiles;        // P / 16
+};
+
 }  // namespace ssm

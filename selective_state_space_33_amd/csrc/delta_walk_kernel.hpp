@@ -39,55 +39,76 @@ struct DeltaStream {
   }
 };
 
-template <int DK> struct DeltaWalkLds {
+template <int DK, bool KEEP> struct DeltaWalkLds {
   __attribute__((aligned(16))) uint16_t k[kDeltaC * kRowLd<DK>];
   __attribute__((aligned(16))) uint16_t kt[kDeltaC * kColLd<DK>];
   __attribute__((aligned(16))) uint16_t q[kDeltaC * kRowLd<DK>];
-  __attribute__((aligned(16))) char img[kImgBytes];
+  __attribute__((aligned(16))) char img[KEEP ? 12 * kFrag + 1024 : kImgBytes];  // KEEP: T and four gates
 };
 
-template <int DK, int W, int NC>
-__global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) {
+// What the backward's walk takes and writes beside the forward's.
+struct DeltaKeep {
+  const void* dy;
+  const float* dfinal;
+  char* state;
+  char* r;
+  float* oterm;
+};
+__device__ __forceinline__ DeltaKeep kept(const DeltaChunkParams&) { return {}; }
+__device__ __forceinline__ DeltaKeep kept(const DeltaBwdParams& b) { return {b.dy, b.dfinal, b.state, b.r, b.oterm}; }
+
+template <bool KEEP> struct DeltaWalkArgs {
+  typedef DeltaChunkParams type;
+};
+template <> struct DeltaWalkArgs<true> {
+  typedef DeltaBwdParams type;
+};
+__device__ __forceinline__ const DeltaChunkParams& chunk_params(const DeltaChunkParams& p) { return p; }
+__device__ __forceinline__ const DeltaChunkParams& chunk_params(const DeltaBwdParams& p) { return p.c; }
+
+// KEEP: the backward's walk over the same chunks.  It stores no y but what the gradients take of each chunk: S0 and R as
+// operand fragments, (S0 q) . dy of each token over this tile's channels, and the largest |dy| of the unit.
+template <int DK, int W, bool KEEP>
+__global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkArgs<KEEP>::type wp) {
+  const DeltaChunkParams& p = chunk_params(wp);
+  const DeltaKeep keep = kept(wp);
   constexpr int KT = DK / 32, DT = DK / 16, NTH = 64 * W;
-  using Lds = DeltaWalkLds<DK>;
+  using Lds = DeltaWalkLds<DK, KEEP>;
+  constexpr int GATES = KEEP ? 12 * kFrag : kImgGrow, IMG = KEEP ? kBwdImgBytes : kImgBytes;
   __shared__ Lds lds[2];
   // each wavefront's own values, [token][channel], as they are in memory (bf16): written with the next chunk's
   // operands, read transposed at its start
-  __shared__ __attribute__((aligned(16))) uint16_t lds_v[W][NC][kDeltaC * 16];
+  __shared__ __attribute__((aligned(16))) uint16_t lds_v[W][kDeltaC * 16];
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t blocks = (p.P + 16 * NC * W - 1) / (16 * NC * W);  // workgroups per unit
+  const int64_t blocks = (p.P + 16 * W - 1) / (16 * W);  // workgroups per unit
   const int64_t id = xcd_order(blockIdx.x, p.rows * p.H * blocks);
   const int64_t unit = id / blocks, seq = unit / p.H, h = unit % p.H, g = h / (p.H / p.G);
-  const int col = static_cast<int>((id % blocks) * W + w) * 16 * NC;  // first channel of this wavefront
+  const int col = static_cast<int>((id % blocks) * W + w) * 16;  // first channel of this wavefront
   const DeltaSeq sq = delta_seq(p.cu, seq, p.L, p.chunks);
   const int nchunks = static_cast<int>((sq.len + kDeltaC - 1) / kDeltaC);
   const int64_t rowe = p.H * p.P, krow = p.G * DK;
   const int rowe32 = static_cast<int>(rowe), krow32 = static_cast<int>(krow);  // the host keeps them below 2^22
   const int yrow = (lr * rowe32 + 4 * lq) * 2;
 
-  // ---- the state: channel col + 16 n + lr, states 16 d + 4 lq .. + 3
-  f32x4_t S[NC][DT];
+  // ---- the state: channel col + lr, states 16 d + 4 lq .. + 3
+  f32x4_t S[DT];
   const int64_t sbase = (unit * p.P + col + lr) * DK + 4 * lq;
 #pragma unroll
-  for (int n = 0; n < NC; ++n)
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      S[n][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.h0 && col + 16 * n < p.P)
-        S[n][d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * n * DK + 16 * d);
-    }
+  for (int d = 0; d < DT; ++d) {
+    S[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.h0 && col < p.P) S[d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * d);
+  }
 
   // ---- chunk loads, one chunk ahead in registers
   constexpr int PIECES = kDeltaC * DK / 8, PER = (PIECES + NTH - 1) / NTH;
-  constexpr int IPIECES = kImgBytes / 16, IPER = (IPIECES + NTH - 1) / NTH;
+  constexpr int IPIECES = sizeof(Lds::img) / 16, IPER = (IPIECES + NTH - 1) / NTH;
   // byte offset of the channel tile: past every resource when the head has no such tile, where loads return zero and
   // stores are dropped (a branch around each load would make the compiler wait for it)
-  int ctile[NC];
-#pragma unroll
-  for (int n = 0; n < NC; ++n) ctile[n] = col + 16 * n < p.P ? (col + 16 * n) * 2 : kPastEnd;
+  const int64_t tiles = p.P / 16;
+  const int ctile = col < p.P ? col * 2 : kPastEnd;
   u32x4_t gk[PER], gq[PER], gi[IPER];
-  u32x2_t gv[NC][4];
+  u32x2_t gv[4];
   // Each tensor's chunks in order, as a base that moves on (computing a chunk's address anew took a hundred scalar
   // instructions a chunk).  Past the last chunk the resources are empty, so the loop loads without a branch: a
   // conditional load's registers would be copied, and waited for, where the paths meet.
@@ -97,16 +118,30 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
   DeltaStream ks(static_cast<const uint16_t*>(p.k) + kb, krow * kDeltaC * 2, ktail);
   DeltaStream qs(static_cast<const uint16_t*>(p.q) + kb, krow * kDeltaC * 2, ktail);
   DeltaStream vs(static_cast<const uint16_t*>(p.v) + vb, rowe * kDeltaC * 2, vtail);
-  DeltaStream ys(static_cast<uint16_t*>(p.y) + vb, rowe * kDeltaC * 2, vtail);
-  DeltaStream is(p.img + (sq.slot * p.H + h) * kImgBytes, p.H * kImgBytes, kImgBytes);
-  // y of a chunk, four consecutive channels of token 16 t + lr in a lane; stored during the chunk after it
-  u32x2_t yo[NC][4];
+  // y of the forward; KEEP: dY
+  DeltaStream ys(static_cast<const uint16_t*>(KEEP ? keep.dy : p.y) + vb, rowe * kDeltaC * 2, vtail);
+  DeltaStream is(p.img + (sq.slot * p.H + h) * IMG, p.H * IMG, IMG);
+  // what KEEP writes of a chunk (these resources cover one tile; a lane of no tile lies behind them)
+  const int64_t cell0 = (sq.slot * p.H + h) * tiles + col / 16, cells = p.H * tiles;
+  DeltaStream ss(keep.state + cell0 * (2 * KT * kFrag), cells * (2 * KT * kFrag), 2 * KT * kFrag);
+  DeltaStream rs(keep.r + cell0 * (4 * kFrag), cells * (4 * kFrag), 4 * kFrag);
+  DeltaStream os(keep.oterm + cell0 * kDeltaC, cells * kDeltaC * 4, kDeltaC * 4);
+  const int mine = lane * 16 + (col < p.P ? 0 : kPastEnd);
+  float amax = 0.0f;
+  // y of a chunk, four consecutive channels of token 16 t + lr in a lane; stored during the chunk after it.  KEEP: dY of
+  // the chunk, in the same places.
+  u32x2_t yo[4];
   // What passes between memory, registers and LDS for a chunk, as ITEMS: the row pieces of K and Q, the image's
   // pieces, the values and y, two token tiles each.  A step of the loop below takes its share of them: piece by piece
   // into LDS what was loaded a chunk ago, and the same piece of the chunk after out of memory.  (All at once they
   // kept the wavefronts waiting for the CU's one memory path: 64 bytes a clock for 83 KB a chunk.)
-  constexpr int ITEMS = PER + IPER + 4 * NC;
-  rsrc_t rk, rq, ri, rv, ry;
+  constexpr int LOADS = PER + IPER + 2, ITEMS = LOADS + (KEEP ? 0 : 2);
+  rsrc_t rk, rq, ri, rv, ry, rkeep;
+  auto load_dy = [&] {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      yo[t] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(ry, yrow + ctile, 32 * t * rowe32, 0));
+  };
   auto next_rsrc = [&](int left) { rk = ks.take(left), rq = qs.take(left), ri = is.take(left), rv = vs.take(left); };
   auto load_item = [&](auto item) {
     constexpr int i = decltype(item)::value;
@@ -117,12 +152,14 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
       gq[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
     } else if constexpr (i < PER + IPER) {
       constexpr int e = i - PER;
-      gi[e] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ri, (tid + NTH * e) * 16, 0, 0));
-    } else if constexpr (i < PER + IPER + 2 * NC) {
-      constexpr int n = (i - PER - IPER) / 2, t = 2 * ((i - PER - IPER) % 2);
-      const int at = yrow + ctile[n];
-      gv[n][t] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rv, at, 32 * t * rowe32, 0));
-      gv[n][t + 1] =
+      // KEEP takes T and the gates, not P between them
+      const int at = (tid + NTH * e) * 16 + (KEEP && tid + NTH * e >= GATES / 16 ? kBwdGates - GATES : 0);
+      gi[e] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ri, at, 0, 0));
+    } else if constexpr (i < PER + IPER + 2) {
+      constexpr int t = 2 * ((i - PER - IPER) % 2);
+      const int at = yrow + ctile;
+      gv[t] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rv, at, 32 * t * rowe32, 0));
+      gv[t + 1] =
           __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rv, at, 32 * (t + 1) * rowe32, 0));
     }
   };
@@ -140,32 +177,34 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
     } else if constexpr (i < PER + IPER) {
       const int e = tid + NTH * (i - PER);
       if (IPIECES % NTH == 0 || e < IPIECES) *reinterpret_cast<u32x4_t*>(&b.img[e * 16]) = gi[i - PER];
-    } else if constexpr (i < PER + IPER + 2 * NC) {
-      constexpr int n = (i - PER - IPER) / 2, t = 2 * ((i - PER - IPER) % 2);
-      *reinterpret_cast<u32x2_t*>(&lds_v[w][n][(16 * t + lr) * 16 + 4 * lq]) = gv[n][t];
-      *reinterpret_cast<u32x2_t*>(&lds_v[w][n][(16 * t + 16 + lr) * 16 + 4 * lq]) = gv[n][t + 1];
+    } else if constexpr (i < PER + IPER + 2) {
+      constexpr int t = 2 * ((i - PER - IPER) % 2);
+      *reinterpret_cast<u32x2_t*>(&lds_v[w][(16 * t + lr) * 16 + 4 * lq]) = gv[t];
+      *reinterpret_cast<u32x2_t*>(&lds_v[w][(16 * t + 16 + lr) * 16 + 4 * lq]) = gv[t + 1];
     } else {
-      constexpr int e = i - PER - IPER - 2 * NC, n = e / 2, t = 2 * (e % 2);
-      __builtin_amdgcn_raw_buffer_store_b64(yo[n][t], ry, yrow + ctile[n], 32 * t * rowe32, 0);
-      __builtin_amdgcn_raw_buffer_store_b64(yo[n][t + 1], ry, yrow + ctile[n], 32 * (t + 1) * rowe32, 0);
+      constexpr int e = i - PER - IPER - 2, t = 2 * (e % 2);
+      __builtin_amdgcn_raw_buffer_store_b64(yo[t], ry, yrow + ctile, 32 * t * rowe32, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(yo[t + 1], ry, yrow + ctile, 32 * (t + 1) * rowe32, 0);
     }
   };
 
   if (nchunks > 0) {
     next_rsrc(nchunks);
-    static_for<ITEMS - 2 * NC>([&](auto i) { load_item(i); });
+    static_for<LOADS>([&](auto i) { load_item(i); });
     next_rsrc(nchunks - 1);
-    static_for<ITEMS - 2 * NC>([&](auto i) {
+    static_for<LOADS>([&](auto i) {
       stage_item(lds[0], i);
       load_item(i);
     });
   }
+  if constexpr (KEEP) {
+    ry = ys.take(nchunks);
+    load_dy();
+  }
   __syncthreads();
-  f16x8_t Sh[NC][KT], Sl[NC][KT];
+  f16x8_t Sh[KT], Sl[KT];
 #pragma unroll
-  for (int n = 0; n < NC; ++n)
-#pragma unroll
-    for (int kk = 0; kk < KT; ++kk) split_f16(S[n][2 * kk], S[n][2 * kk + 1], Sh[n][kk], Sl[n][kk]);
+    for (int kk = 0; kk < KT; ++kk) split_f16(S[2 * kk], S[2 * kk + 1], Sh[kk], Sl[kk]);
   for (int c = 0; c < nchunks; ++c) {
     const Lds& b = lds[c & 1];
     Lds& next = lds[(c + 1) & 1];
@@ -186,18 +225,21 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
     };
     f16x8_t th[6], tl[6];
     auto read_t = [&](int f) { th[f] = img_frag(kImgThi, f), tl[f] = img_frag(kImgTlo, f); };
-    u32x2_t vq[NC][4];
-    const float fade = *reinterpret_cast<const float*>(&b.img[kImgGrow + (kDeltaC - 1) * 4]);
+    u32x2_t vq[4];
+    const float fade = *reinterpret_cast<const float*>(&b.img[GATES + (kDeltaC - 1) * 4]);
 #pragma unroll
     for (int j = 0; j < 3; ++j) read_step(j);
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) vq[n][t] = lds_tr4(&lds_v[w][n][(16 * t + 4 * lq + (lr >> 2)) * 16 + 4 * (lr & 3)]);
+      for (int t = 0; t < 4; ++t) vq[t] = lds_tr4(&lds_v[w][(16 * t + 4 * lq + (lr >> 2)) * 16 + 4 * (lr & 3)]);
     __builtin_amdgcn_sched_barrier(0);
     next_rsrc(nchunks - c - 2);
-    ry = ys.take(c > 0 ? 2 : 0);  // of the chunk before, which is whole
-    if (c == 0) ys.base -= ys.step;
+    if constexpr (KEEP) {
+      ry = ys.take(nchunks - c - 1);
+      rkeep = ss.take(1);
+    } else {
+      ry = ys.take(c > 0 ? 2 : 0);  // of the chunk before, which is whole
+      if (c == 0) ys.base -= ys.step;
+    }
     // this chunk's share of ITEMS, in slots evenly spread over its products
     constexpr int SLOTS = STEPS + 3 + 2 * KT;
     auto slot = [&](auto place) {
@@ -208,16 +250,13 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
       });
       __builtin_amdgcn_sched_barrier(0);
     };
-    f32x4_t x[NC][4], o[NC][4], grow[2];
-    f16x8_t Xh[NC][2], Xl[NC][2];
+    f32x4_t x[4], o[4], grow[2];
+    f16x8_t Xh[2], Xl[2];
     auto finish_x = [&](int t) {
+      const float v[4] = {bf16_lo(vq[t][0]), bf16_hi(vq[t][0]), bf16_lo(vq[t][1]), bf16_hi(vq[t][1])};
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        const float v[4] = {bf16_lo(vq[n][t][0]), bf16_hi(vq[n][t][0]), bf16_lo(vq[n][t][1]), bf16_hi(vq[n][t][1])};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[n][t][r] = __builtin_fmaf(-grow[t & 1][r], x[n][t][r], v[r]);
-        if (t & 1) split_f16(x[n][t - 1], x[n][t], Xh[n][t >> 1], Xl[n][t >> 1]);
-      }
+      for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(-grow[t & 1][r], x[t][r], v[r]);
+      if (t & 1) split_f16(x[t - 1], x[t], Xh[t >> 1], Xl[t >> 1]);
     };
     static_for<STEPS>([&](auto step) {
       constexpr int j = decltype(step)::value, t = j / KT, kk = j % KT;
@@ -225,21 +264,21 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
         read_step(j + 3);
       else
         read_t(j + 3 - STEPS);
-      if (kk == KT - 1) grow[t & 1] = img_vec(kImgGrow, t);
+      if (kk == KT - 1) grow[t & 1] = img_vec(GATES, t);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        if (kk == 0) x[n][t] = o[n][t] = zero;
-        x[n][t] = mfma_f16(kf[j & 3], Sl[n][kk], x[n][t]);
-        o[n][t] = mfma_f16(Sh[n][kk], qf[j & 3], o[n][t]);
-        x[n][t] = mfma_f16(kf[j & 3], Sh[n][kk], x[n][t]);
-      }
+      if (kk == 0) x[t] = o[t] = zero;
+      x[t] = mfma_f16(kf[j & 3], Sl[kk], x[t]);
+      o[t] = mfma_f16(Sh[kk], qf[j & 3], o[t]);
+      x[t] = mfma_f16(kf[j & 3], Sh[kk], x[t]);
+      // (S0 q) . dy goes into the gradient of a fade, which needs both parts of S0
+      if constexpr (KEEP) o[t] = mfma_f16(Sl[kk], qf[j & 3], o[t]);
+      if constexpr (KEEP && j < 2 * KT)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, j < KT ? Sh[j] : Sl[j - KT]), rkeep, mine,
+                                               j * kFrag, 0);
       if constexpr (kk == 0 && t > 0) finish_x(t - 1);
       // the state itself (its operands are copies) fades here, out of the chain
 #pragma unroll
-      for (int d = j * DT / STEPS; d < (j + 1) * DT / STEPS; ++d)
-#pragma unroll
-        for (int n = 0; n < NC; ++n) S[n][d] *= fade;
+      for (int d = j * DT / STEPS; d < (j + 1) * DT / STEPS; ++d) S[d] *= fade;
       slot(IC<j>{});
     });
     finish_x(3);
@@ -250,20 +289,20 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
     read_t(5);
     f32x4_t left[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) left[t] = img_vec(kImgLeft, t);
+    for (int t = 0; t < 4; ++t) {
+      left[t] = img_vec(GATES + 512, t);
+      if constexpr (KEEP) left[t] *= img_vec(GATES + 768, t);
+    }
     f16x8_t kc[DT];  // K^T, a half of the tokens at a time
 #pragma unroll
     for (int d = 0; d < DT; ++d) kc[d] = lds_col_frag<DK>(b.kt, 0, d, lr, lq);
     __builtin_amdgcn_sched_barrier(0);
-    f32x4_t u[NC][4];
+    f32x4_t u[4];
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) u[n][t] = zero;
+    for (int t = 0; t < 4; ++t) u[t] = zero;
     auto t_product = [&](int t, int m, int i) {
       const int f = frag_of(t, m);
-#pragma unroll
-      for (int n = 0; n < NC; ++n) u[n][t] = mfma_f16(i == 2 ? tl[f] : th[f], i == 1 ? Xl[n][m] : Xh[n][m], u[n][t]);
+      u[t] = mfma_f16(i == 2 ? tl[f] : th[f], i == 1 ? Xl[m] : Xh[m], u[t]);
     };
     static_for<3>([&](auto i) {
       t_product(0, 0, i.value);
@@ -273,21 +312,17 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
       slot(IC<STEPS + decltype(i)::value>{});
     });
     // ---- S = e^{cs_C} S + K^T diag(e^{cs_C - cs} b) R
-    f16x8_t Uh[NC][2], Ul[NC][2];
+    f16x8_t Uh[2], Ul[2];
     static_for<3>([&](auto i) {
       t_product(2, 1, i.value);
       t_product(3, 1, i.value);
     });
-#pragma unroll
-    for (int n = 0; n < NC; ++n) split_f16(u[n][0] * left[0], u[n][1] * left[1], Uh[n][0], Ul[n][0]);
+    split_f16(u[0] * left[0], u[1] * left[1], Uh[0], Ul[0]);
     auto state_product = [&](int d, int m) {
-#pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        S[n][d] = mfma_f16(kc[d], Uh[n][m], S[n][d]);
-        S[n][d + 1] = mfma_f16(kc[d + 1], Uh[n][m], S[n][d + 1]);
-        S[n][d] = mfma_f16(kc[d], Ul[n][m], S[n][d]);
-        S[n][d + 1] = mfma_f16(kc[d + 1], Ul[n][m], S[n][d + 1]);
-      }
+      S[d] = mfma_f16(kc[d], Uh[m], S[d]);
+      S[d + 1] = mfma_f16(kc[d + 1], Uh[m], S[d + 1]);
+      S[d] = mfma_f16(kc[d], Ul[m], S[d]);
+      S[d + 1] = mfma_f16(kc[d + 1], Ul[m], S[d + 1]);
     };
     static_for<KT>([&](auto k) {
       constexpr int d = 2 * decltype(k)::value;
@@ -296,55 +331,98 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(DeltaChunkParams p) 
       kc[d + 1] = lds_col_frag<DK>(b.kt, 32, d + 1, lr, lq);
       slot(IC<STEPS + 3 + decltype(k)::value>{});
     });
-    f16x8_t Rf[NC][2];
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      split_f16(u[n][2] * left[2], u[n][3] * left[3], Uh[n][1], Ul[n][1]);
-      Rf[n][0] = pair_f16(u[n][0], u[n][1]), Rf[n][1] = pair_f16(u[n][2], u[n][3]);
-    }
-    f16x8_t pf[6];
+    f16x8_t Rf[2];
+    split_f16(u[2] * left[2], u[3] * left[3], Uh[1], Ul[1]);
+    f16x8_t pf[KEEP ? 1 : 6];
     float og[4];
+    if constexpr (KEEP) {
+      rkeep = rs.take(1);
+      f16x8_t Rl;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) og[t] = *reinterpret_cast<const float*>(&b.img[kImgOut + (16 * t + lr) * 4]);
+      for (int m = 0; m < 2; ++m) {
+        split_f16(u[2 * m], u[2 * m + 1], Rf[m], Rl);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Rf[m]), rkeep, mine, m * kFrag, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Rl), rkeep, mine, (2 + m) * kFrag, 0);
+      }
+      og[0] = *reinterpret_cast<const float*>(&b.img[GATES + 256 + lane * 4]);
+    } else {
+      Rf[0] = pair_f16(u[0], u[1]), Rf[1] = pair_f16(u[2], u[3]);
 #pragma unroll
-    for (int f = 0; f < 6; ++f) pf[f] = img_frag(kImgP, f);
+      for (int t = 0; t < 4; ++t) og[t] = *reinterpret_cast<const float*>(&b.img[kImgOut + (16 * t + lr) * 4]);
+#pragma unroll
+      for (int f = 0; f < 6; ++f) pf[f] = img_frag(kImgP, f);
+    }
     __builtin_amdgcn_sched_barrier(0);
     // the next chunk's operands of the state are split under the products of the following tiles
     static_for<KT>([&](auto k) {
       constexpr int kk = decltype(k)::value, d = 2 * kk;
       state_product(d, 1);
-      if constexpr (kk > 0) {
-#pragma unroll
-        for (int n = 0; n < NC; ++n) split_f16(S[n][d - 2], S[n][d - 1], Sh[n][kk - 1], Sl[n][kk - 1]);
-      }
+      if constexpr (kk > 0) split_f16(S[d - 2], S[d - 1], Sh[kk - 1], Sl[kk - 1]);
       slot(IC<STEPS + 3 + KT + kk>{});
     });
-    // ---- Y^T = (Q S0)^T diag(scale e^cs) + R^T P^T
+    if constexpr (KEEP) {
+      // (S0 q) . dy over these 16 channels: token 16 t + lr's four channels of each lane group, then the groups
+      float dots[4];
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
+      for (int t = 0; t < 4; ++t) {
+        const float d[4] = {bf16_lo(yo[t][0]), bf16_hi(yo[t][0]), bf16_lo(yo[t][1]), bf16_hi(yo[t][1])};
+        dots[t] = 0.0f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) o[n][t] *= og[t];
+        for (int r = 0; r < 4; ++r) {
+          dots[t] = __builtin_fmaf(o[t][r], d[r], dots[t]);
+          amax = __builtin_fmaxf(amax, __builtin_fabsf(d[r]));
+        }
+      }
+      split_f16(S[DT - 2], S[DT - 1], Sh[KT - 1], Sl[KT - 1]);
+      load_dy();
+      // lane 16 lq + lr ends with token 16 lq + lr
+      const bool odd = lq & 1, high = lq & 2;
+      const float a0 = (odd ? dots[1] : dots[0]) + __shfl_xor(odd ? dots[0] : dots[1], 16, 64);
+      const float a1 = (odd ? dots[3] : dots[2]) + __shfl_xor(odd ? dots[2] : dots[3], 16, 64);
+      const float dot = (high ? a1 : a0) + __shfl_xor(high ? a0 : a1, 32, 64);
+      rkeep = os.take(1);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot * og[0]), rkeep, lane * 4 + (col < p.P ? 0 : kPastEnd),
+                                            0, 0);
+    } else {
+      // ---- Y^T = (Q S0)^T diag(scale e^cs) + R^T P^T
 #pragma unroll
-      for (int t = 0; t < 4; ++t) o[n][t] = mfma_f16(Rf[n][0], pf[frag_of(t, 0)], o[n][t]);
+      for (int t = 0; t < 4; ++t) o[t] *= og[t];
 #pragma unroll
-      for (int t = 2; t < 4; ++t) o[n][t] = mfma_f16(Rf[n][1], pf[frag_of(t, 1)], o[n][t]);
-      split_f16(S[n][DT - 2], S[n][DT - 1], Sh[n][KT - 1], Sl[n][KT - 1]);
+      for (int t = 0; t < 4; ++t) o[t] = mfma_f16(Rf[0], pf[frag_of(t, 0)], o[t]);
+#pragma unroll
+      for (int t = 2; t < 4; ++t) o[t] = mfma_f16(Rf[1], pf[frag_of(t, 1)], o[t]);
+      split_f16(S[DT - 2], S[DT - 1], Sh[KT - 1], Sl[KT - 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        yo[n][t] = u32x2_t{pack_bf16x2(o[n][t][0], o[n][t][1]), pack_bf16x2(o[n][t][2], o[n][t][3])};
+        yo[t] = u32x2_t{pack_bf16x2(o[t][0], o[t][1]), pack_bf16x2(o[t][2], o[t][3])};
     }
     __syncthreads();
   }
-  if (nchunks > 0) {
-    ry = ys.take(1);
-    static_for<2 * NC>([&](auto i) { stage_item(lds[0], IC<ITEMS - 2 * NC + decltype(i)::value>{}); });
-  }
-  if (p.hT) {
+  if constexpr (KEEP) {
+    if (nchunks > 0 && col < p.P) {
+      if (keep.dfinal) {
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
+        for (int d = 0; d < DT; ++d) {
+          const f32x4_t f = *reinterpret_cast<const f32x4_t*>(keep.dfinal + sbase + 16 * d);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[r]));
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 64));
+      // a maximum does not depend on the order of its arguments, so neither does the scale
+      if (lane == 0) atomicMax(p.amax + unit, __float_as_uint(amax));
+    }
+  } else {
+    if (nchunks > 0) {
+      ry = ys.take(1);
+      static_for<2>([&](auto i) { stage_item(lds[0], IC<LOADS + decltype(i)::value>{}); });
+    }
+    if (p.hT) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        if (col + 16 * n < p.P) *reinterpret_cast<f32x4_t*>(p.hT + sbase + 16 * n * DK + 16 * d) = S[n][d];
+        if (col < p.P) *reinterpret_cast<f32x4_t*>(p.hT + sbase + 16 * d) = S[d];
+    }
   }
 }
 

@@ -87,10 +87,10 @@ template <int DK> hipError_t run_chunked(DeltaChunkParams& p, hipStream_t s) {
   // 2.8 us a chunk), else eight, which share a head's staging (3.4 us a chunk for twice the channels).
   const int64_t small = units * ((tiles + 3) / 4);
   if (tiles > 4 && small > device_cu_count())
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 8, 1>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))), dim3(512),
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 8, false>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))), dim3(512),
                        0, s, p);
   else
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, 1>), dim3(static_cast<unsigned>(small)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, false>), dim3(static_cast<unsigned>(small)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

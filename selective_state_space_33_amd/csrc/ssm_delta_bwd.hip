@@ -55,7 +55,12 @@ template <int DK> hipError_t run_bwd(const DeltaBwdParams& bp, hipStream_t s) {
   hipLaunchKernelGGL((delta_prep_kernel<DK, true>), dim3(cells), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((delta_bwd_walk_kernel<DK, W, false>), dim3(walks), dim3(64 * W), 0, s, bp);
+  // (eight or four wavefronts a workgroup as in the forward)
+  if (bp.tiles > 4 && walks > static_cast<unsigned>(device_cu_count()))
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 8, true>), dim3(static_cast<unsigned>(p.rows * p.H * ((bp.tiles + 7) / 8))),
+                       dim3(512), 0, s, bp);
+  else
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, true>), dim3(walks), dim3(256), 0, s, bp);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((delta_bwd_walk_kernel<DK, W, true>), dim3(walks), dim3(64 * W), 0, s, bp);
