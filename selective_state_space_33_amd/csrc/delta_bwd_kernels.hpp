@@ -48,38 +48,37 @@ __device__ __forceinline__ float grad_scale(unsigned amax_bits) {
   return __uint_as_float(static_cast<unsigned>(s + 127) << 23);
 }
 
-constexpr int kSkew = 320;               // bytes of a fragment's 16 lanes in LDS
-constexpr int kSkewFrag = 4 * kSkew;     // (four column runs of a transposed read then lie on distinct banks)
-constexpr int kBwdLdsImg = 24 * kSkewFrag + 1536;
-
-// The image from registers into LDS, fragments skewed.
-template <int NTH, int IPER> __device__ __forceinline__ void stage_bwd_img(char* img, const u32x4_t (&gi)[IPER]) {
+// bf16 values as floats, times a scale.
+__device__ __forceinline__ f32x4_t bf16x4_f32(u32x2_t v, float s) {
+  return f32x4_t{bf16_lo(v[0]) * s, bf16_hi(v[0]) * s, bf16_lo(v[1]) * s, bf16_hi(v[1]) * s};
+}
+// acc + v * (hi + lo) of a pair, element by element.
+__device__ __forceinline__ f32x4_t fma_pair(f32x4_t v, f16x4_t hi, f16x4_t lo, f32x4_t acc) {
 #pragma unroll
-  for (int i = 0; i < IPER; ++i) {
-    const int e = threadIdx.x + NTH * i;
-    if (e >= kBwdImgBytes / 16) continue;
-    const int f = e >> 6, ln = e & 63;
-    const int at = f < 24 ? f * kSkewFrag + (ln >> 4) * kSkew + (ln & 15) * 16 : 24 * kSkewFrag + (e - 24 * 64) * 16;
-    *reinterpret_cast<u32x4_t*>(img + at) = gi[i];
+  for (int r = 0; r < 4; ++r)
+    acc[r] = __builtin_fmaf(v[r], static_cast<float>(hi[r]), __builtin_fmaf(v[r], static_cast<float>(lo[r]), acc[r]));
+  return acc;
+}
+
+// Sums of sixteen values over the 16 lanes of a row: lane lr receives the sum of value lr.  Each step exchanges the half
+// of the values that the partner keeps; the masks 15, 7, 2, 1 are the lane permutations a DPP row has.
+template <int CTRL> __device__ __forceinline__ float dpp_move(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum_rows16(const f32x4_t (&v)[4], int lr) {
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float lo = v[i >> 2][i & 3], hi = v[2 + (i >> 2)][i & 3];
+    a[i] = (lr & 8 ? hi : lo) + dpp_move<0x140>(lr & 8 ? lo : hi);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = (lr & 4 ? a[i + 4] : a[i]) + dpp_move<0x141>(lr & 4 ? a[i] : a[i + 4]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) c[i] = (lr & 2 ? b[i + 2] : b[i]) + dpp_move<0x4e>(lr & 2 ? b[i] : b[i + 2]);
+  return (lr & 1 ? c[1] : c[0]) + dpp_move<0xb1>(lr & 1 ? c[0] : c[1]);
 }
-__device__ __forceinline__ f16x8_t bwd_row_frag(const char* img, int f, int lr, int lq) {
-  return *reinterpret_cast<const f16x8_t*>(img + f * kSkewFrag + lq * kSkew + lr * 16);
-}
-// The transpose's fragment: K index the rows 32 m .. + 31 of the matrix whose fragments start at f0, columns 16 ct + lr.
-__device__ __forceinline__ f16x8_t bwd_col_frag(const char* img, int f0, int ct, int m, int lr, int lq) {
-  const int at = (lr & 3) * kSkew + (4 * lq + (lr >> 2)) * 16 + (ct & 1) * 8;
-  const u32x2_t a = lds_tr4(reinterpret_cast<const uint16_t*>(img + (f0 + frag_of(2 * m, ct >> 1)) * kSkewFrag + at));
-  const u32x2_t b =
-      lds_tr4(reinterpret_cast<const uint16_t*>(img + (f0 + frag_of(2 * m + 1, ct >> 1)) * kSkewFrag + at));
-  return __builtin_bit_cast(f16x8_t, u32x4_t{a[0], a[1], b[0], b[1]});
-}
-__device__ __forceinline__ f32x4_t bwd_gate(const char* img, int base, int t, int lq) {
-  return *reinterpret_cast<const f32x4_t*>(img + 24 * kSkewFrag + (base - kBwdGates) + (16 * t + 4 * lq) * 4);
-}
-__device__ __forceinline__ float bwd_gate1(const char* img, int base, int t) {
-  return *reinterpret_cast<const float*>(img + 24 * kSkewFrag + (base - kBwdGates) + t * 4);
-}
+
 // A fragment of rows (paired order) of an array stored plain.
 template <int LD> __device__ __forceinline__ f16x8_t plain_row_frag(const uint16_t* base, int r, int kk, int lq) {
   const uint16_t* a = base + r * LD + 32 * kk + 4 * lq;
@@ -87,369 +86,368 @@ template <int LD> __device__ __forceinline__ f16x8_t plain_row_frag(const uint16
   return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
 }
 
-// bf16 values as floats, times a scale.
-__device__ __forceinline__ f32x4_t bf16x4_f32(u32x2_t v, float s) {
-  return f32x4_t{bf16_lo(v[0]) * s, bf16_hi(v[0]) * s, bf16_lo(v[1]) * s, bf16_hi(v[1]) * s};
-}
+// A tensor's chunks from the last one back, as DeltaStream the other way.
+struct DeltaBackStream {
+  char* base;
+  int64_t step;
+  int size, full;
+  // the chunk at p (of `last` bytes) first, then those before it, `chunk` bytes apart and `whole` long
+  __device__ __forceinline__ DeltaBackStream(const void* p, int64_t chunk, int64_t last, int64_t whole)
+      : base(static_cast<char*>(const_cast<void*>(p))),
+        step(chunk),
+        size(static_cast<int>(last)),
+        full(static_cast<int>(whole)) {}
+  __device__ __forceinline__ rsrc_t take(bool go) {
+    const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(base, 0, go ? size : 0, kBufWord3);
+    base -= go ? step : 0;
+    size = go ? full : size;
+    return r;
+  }
+};
 
-// Sum over the four lane groups of 16 (lanes lr, 16 + lr, ...), in all of them.
-__device__ __forceinline__ float sum_groups(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
-}
-// Sum of each component over the 16 lanes lr of a group, in all of them.
-__device__ __forceinline__ f32x4_t sum_lanes16(f32x4_t v) {
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] += __shfl_xor(v[r], o, 64);
-  return v;
-}
-__device__ __forceinline__ float sum_wave(float v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
+template <int DK> struct DeltaBackLds {
+  __attribute__((aligned(16))) uint16_t k[kDeltaC * kColLd<DK>];
+  __attribute__((aligned(16))) uint16_t q[kDeltaC * kColLd<DK>];
+  __attribute__((aligned(16))) char img[24 * kFrag + 1024];  // the transposes of T and P0 (pairs) and four gates
+};
 
-// Walks forward (BACK false) keeping S0, R and y . dy, or back (BACK true) with the adjoint.  One tile of 16 channels a
-// wavefront, W of them a workgroup sharing the chunk in LDS.
-template <int DK, int W, bool BACK>
-__global__ void __launch_bounds__(64 * W) delta_bwd_walk_kernel(DeltaBwdParams bp) {
+// The walk back with the adjoint.  As delta_walk_kernel, a wavefront owns 16 channels and the chunk's operands are staged
+// a chunk ahead, item by item between the products.  Per chunk (dstate 128) 176 MFMAs: K dS and K S0 32 each, P0^T dY 12,
+// <dS, S0> 12, T^T (b Y0) 18 and 6 for dV's rows, Q^T dY 32, K^T dV 32.  The chain is K dS -> b Y0 -> dV -> K^T dV; the
+// rest fills it.  S0 and R are loaded for the chunk before as soon as this chunk has read them.
+template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_walk_kernel(DeltaBwdParams bp) {
   const DeltaChunkParams& p = bp.c;
-  constexpr int KT = DK / 32, DT = DK / 16, NTH = 64 * W;
-  __shared__ __attribute__((aligned(16))) uint16_t sK[kDeltaC * kColLd<DK>];
-  __shared__ __attribute__((aligned(16))) uint16_t sQ[kDeltaC * kColLd<DK>];
-  __shared__ __attribute__((aligned(16))) char sImg[kBwdLdsImg];
-  __shared__ __attribute__((aligned(16))) uint16_t sT[W][kDeltaC * 16];  // forward: V, back: dY, of each wavefront
+  constexpr int KT = DK / 32, DT = DK / 16, NTH = 64 * W, CL = kColLd<DK>;
+  using Lds = DeltaBackLds<DK>;
+  constexpr int GATES = 24 * kFrag;
+  __shared__ Lds lds[2];
+  __shared__ __attribute__((aligned(16))) uint16_t lds_y[W][kDeltaC * 16];  // each wavefront's dY, [token][channel]
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t blocks = (p.P + 16 * W - 1) / (16 * W);
   const int64_t id = xcd_order(blockIdx.x, p.rows * p.H * blocks);
   const int64_t unit = id / blocks, seq = unit / p.H, h = unit % p.H, g = h / (p.H / p.G);
-  const int tile = static_cast<int>((id % blocks) * W + w), col = tile * 16;
-  const bool mine = col < p.P;
+  const int col = static_cast<int>((id % blocks) * W + w) * 16;
   const DeltaSeq sq = delta_seq(p.cu, seq, p.L, p.chunks);
   const int nchunks = static_cast<int>((sq.len + kDeltaC - 1) / kDeltaC);
   const int64_t rowe = p.H * p.P, krow = p.G * DK;
   const int rowe32 = static_cast<int>(rowe), krow32 = static_cast<int>(krow);
   const int yrow = (lr * rowe32 + 4 * lq) * 2;
-  const int ctile = mine ? col * 2 : kPastEnd;
-  const float sc = BACK && nchunks > 0 ? grad_scale(p.amax[unit]) : 1.0f, inv = 1.0f / sc;
+  const float sc = nchunks > 0 ? grad_scale(p.amax[unit]) : 1.0f, inv = 1.0f / sc;
 
-  // ---- forward: S; back: dS (scaled).  Channel col + lr, states 16 d + 4 lq .. + 3
+  // ---- dS (scaled): channel col + lr, states 16 d + 4 lq .. + 3
   f32x4_t S[DT];
   const int64_t sbase = (unit * p.P + col + lr) * DK + 4 * lq;
-  const float* first = BACK ? bp.dfinal : p.h0;
 #pragma unroll
   for (int d = 0; d < DT; ++d) {
     S[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (first && mine) S[d] = *reinterpret_cast<const f32x4_t*>(first + sbase + 16 * d);
-    if constexpr (BACK) S[d] *= sc;
+    if (bp.dfinal && col < p.P) S[d] = *reinterpret_cast<const f32x4_t*>(bp.dfinal + sbase + 16 * d) * sc;
   }
-  float amax = 0.0f;
 
+  // ---- chunk loads, one chunk ahead in registers (items and resources as in delta_walk_kernel)
   constexpr int PIECES = kDeltaC * DK / 8, PER = (PIECES + NTH - 1) / NTH;
-  constexpr int IPIECES = kBwdImgBytes / 16, IPER = (IPIECES + NTH - 1) / NTH;
+  constexpr int IPIECES = sizeof(Lds::img) / 16, IPER = (IPIECES + NTH - 1) / NTH;
+  const bool has = col < p.P;
+  const int ctile = has ? col * 2 : kPastEnd, mine = lane * 16 + (has ? 0 : kPastEnd);
+  const int mine4 = lane * 4 + (has ? 0 : kPastEnd);
+  // where lane (lq, lr) puts the sum of sum_rows16's value lr, which belongs to token 16 (lr / 4) + 4 lq + lr % 4
+  const int term_at = (16 * (lr >> 2) + 4 * lq + (lr & 3)) * 4 + (has ? 0 : kPastEnd);
+  const int64_t lastc = nchunks - 1, ltok = sq.tok + lastc * kDeltaC, last = sq.len - lastc * kDeltaC;
+  const int64_t kb = ltok * krow + g * DK, vb = ltok * rowe + h * p.P;
+  const int64_t kstep = krow * kDeltaC * 2, vstep = rowe * kDeltaC * 2;
+  const int64_t ktail = ((last - 1) * krow + DK) * 2, kfull = ((kDeltaC - 1) * krow + DK) * 2;
+  const int64_t vtail = ((last - 1) * rowe + p.P) * 2, vfull = ((kDeltaC - 1) * rowe + p.P) * 2;
+  const int64_t lcell = (sq.slot + lastc) * p.H + h, tcell = lcell * bp.tiles + col / 16, tcells = p.H * bp.tiles;
+  DeltaBackStream ks(static_cast<const uint16_t*>(p.k) + kb, kstep, ktail, kfull);
+  DeltaBackStream qs(static_cast<const uint16_t*>(p.q) + kb, kstep, ktail, kfull);
+  DeltaBackStream ys(static_cast<const uint16_t*>(bp.dy) + vb, vstep, vtail, vfull);
+  DeltaBackStream os(static_cast<const uint16_t*>(bp.dv) + vb, vstep, vtail, vfull);
+  DeltaBackStream is(p.img + lcell * kBwdImgBytes + kBwdBack, p.H * kBwdImgBytes, sizeof(Lds::img), sizeof(Lds::img));
+  auto tile_stream = [&](const void* base, int bytes) {
+    return DeltaBackStream(static_cast<const char*>(base) + tcell * bytes, tcells * bytes, bytes, bytes);
+  };
+  DeltaBackStream ss = tile_stream(bp.state, 2 * KT * kFrag), rs = tile_stream(bp.r, 4 * kFrag);
+  DeltaBackStream as = tile_stream(bp.adj, KT * kFrag), vs = tile_stream(bp.dvh, 4 * kFrag);
+  DeltaBackStream ls = tile_stream(bp.lterm, kDeltaC * 4), gs = tile_stream(bp.gterm, kDeltaC * 4);
+  DeltaBackStream es = tile_stream(bp.edge, kDeltaC * 4);
   u32x4_t gk[PER], gq[PER], gi[IPER];
-  u32x2_t gv[4], gd[4];
-  f16x8_t gs[BACK ? 2 * KT : 1], gr[BACK ? 4 : 1];  // back: the chunk's S0 and R
-  auto load = [&](int c) {
-    const int64_t c0 = static_cast<int64_t>(c) * kDeltaC, tok = sq.tok + c0;
-    const bool some = c >= 0 && c < nchunks;
-    const int nt = static_cast<int>(sq.len - c0 < kDeltaC ? sq.len - c0 : kDeltaC);
-    const int64_t kb = tok * krow + g * DK, kbytes = some ? ((nt - 1) * krow + DK) * 2 : 0;
-    const int64_t vb = tok * rowe + h * p.P, vbytes = some ? ((nt - 1) * rowe + p.P) * 2 : 0;
-    const rsrc_t rk = make_rsrc(static_cast<const uint16_t*>(p.k) + kb, kbytes);
-    const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(p.q) + kb, kbytes);
-    const rsrc_t ri = make_rsrc(p.img + ((sq.slot + c) * p.H + h) * kBwdImgBytes, some ? kBwdImgBytes : 0);
-    const rsrc_t rv = make_rsrc(static_cast<const uint16_t*>(p.v) + vb, vbytes);
-    const rsrc_t rd = make_rsrc(static_cast<const uint16_t*>(bp.dy) + vb, vbytes);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
+  u32x2_t gd[4], yo[4];  // dY of the next chunk; dV of the last, stored during this one
+  f16x8_t s0[2 * KT], r0[4];
+  constexpr int LOADS = PER + IPER + 2, ITEMS = LOADS + 2;
+  rsrc_t rk, rq, ri, ry, ro, rs0, rr0;
+  auto next_rsrc = [&](bool go) { rk = ks.take(go), rq = qs.take(go), ri = is.take(go), ry = ys.take(go); };
+  auto load_item = [&](auto item) {
+    constexpr int i = decltype(item)::value;
+    if constexpr (i < PER) {
       const int e = tid + NTH * i;
       const int off = (e / (DK / 8)) * krow32 * 2 + (e % (DK / 8)) * 16;
       gk[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0));
       gq[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
-    }
-#pragma unroll
-    for (int i = 0; i < IPER; ++i)
-      gi[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ri, (tid + NTH * i) * 16, 0, 0));
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      gv[t] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rv, yrow + ctile, 32 * t * rowe32, 0));
-      gd[t] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rd, yrow + ctile, 32 * t * rowe32, 0));
-    }
-    if constexpr (BACK) {
-      const int64_t at = ((sq.slot + c) * p.H + h) * bp.tiles + tile;
-      const rsrc_t rs = make_rsrc(bp.state + at * (2 * KT * kFrag), some && mine ? 2 * KT * kFrag : 0);
-      const rsrc_t rr = make_rsrc(bp.r + at * (4 * kFrag), some && mine ? 4 * kFrag : 0);
-#pragma unroll
-      for (int i = 0; i < 2 * KT; ++i)
-        gs[i] = __builtin_bit_cast(f16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, i * kFrag, 0));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        gr[i] = __builtin_bit_cast(f16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rr, lane * 16, i * kFrag, 0));
+    } else if constexpr (i < PER + IPER) {
+      constexpr int e = i - PER;
+      gi[e] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ri, (tid + NTH * e) * 16, 0, 0));
+    } else if constexpr (i < LOADS) {
+      constexpr int t = 2 * (i - PER - IPER);
+      const int at = yrow + ctile;
+      gd[t] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(ry, at, 32 * t * rowe32, 0));
+      gd[t + 1] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(ry, at, 32 * (t + 1) * rowe32, 0));
     }
   };
+  auto stage_item = [&](Lds& b, auto item) {
+    constexpr int i = decltype(item)::value;
+    if constexpr (i < PER) {
+      const int e = tid + NTH * i, at = (e / (DK / 8)) * CL + (e % (DK / 8)) * 8;
+      if (PIECES % NTH == 0 || e < PIECES) {
+        *reinterpret_cast<u32x4_t*>(&b.k[at]) = bf16x8_as_f16(gk[i]);
+        *reinterpret_cast<u32x4_t*>(&b.q[at]) = bf16x8_as_f16(gq[i]);
+      }
+    } else if constexpr (i < PER + IPER) {
+      const int e = tid + NTH * (i - PER);
+      if (IPIECES % NTH == 0 || e < IPIECES) *reinterpret_cast<u32x4_t*>(&b.img[e * 16]) = gi[i - PER];
+    } else if constexpr (i < LOADS) {
+      constexpr int t = 2 * (i - PER - IPER);
+      *reinterpret_cast<u32x2_t*>(&lds_y[w][(16 * t + lr) * 16 + 4 * lq]) = gd[t];
+      *reinterpret_cast<u32x2_t*>(&lds_y[w][(16 * t + 16 + lr) * 16 + 4 * lq]) = gd[t + 1];
+    } else {
+      constexpr int t = 2 * (i - LOADS);
+      __builtin_amdgcn_raw_buffer_store_b64(yo[t], ro, yrow + ctile, 32 * t * rowe32, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(yo[t + 1], ro, yrow + ctile, 32 * (t + 1) * rowe32, 0);
+    }
+  };
+  auto load_s0 = [&](int kk) {
+    s0[kk] = __builtin_bit_cast(f16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rs0, mine, kk * kFrag, 0));
+    s0[KT + kk] = __builtin_bit_cast(f16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rs0, mine, (KT + kk) * kFrag, 0));
+  };
+  auto load_r = [&](int m) {
+    r0[m] = __builtin_bit_cast(f16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rr0, mine, m * kFrag, 0));
+    r0[2 + m] = __builtin_bit_cast(f16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rr0, mine, (2 + m) * kFrag, 0));
+  };
 
+  if (nchunks > 0) {
+    next_rsrc(true);
+    static_for<LOADS>([&](auto i) { load_item(i); });
+    rs0 = ss.take(true), rr0 = rs.take(true);
+    static_for<KT>([&](auto kk) { load_s0(kk.value); });
+    load_r(0);
+    load_r(1);
+    next_rsrc(nchunks > 1);
+    static_for<LOADS>([&](auto i) {
+      stage_item(lds[0], i);
+      load_item(i);
+    });
+  }
+  __syncthreads();
   f16x8_t Sh[KT], Sl[KT];
 #pragma unroll
   for (int kk = 0; kk < KT; ++kk) split_f16(S[2 * kk], S[2 * kk + 1], Sh[kk], Sl[kk]);
-  load(BACK ? nchunks - 1 : 0);
   for (int i = 0; i < nchunks; ++i) {
-    const int c = BACK ? nchunks - 1 - i : i;
-    const int64_t c0 = static_cast<int64_t>(c) * kDeltaC, tok = sq.tok + c0;
-    const int nt = static_cast<int>(sq.len - c0 < kDeltaC ? sq.len - c0 : kDeltaC);
-    const int64_t cell = (sq.slot + c) * p.H + h;  // this chunk's place in the workspace
-    __syncthreads();                               // the last chunk's operands are read
-#pragma unroll
-    for (int e0 = 0; e0 < PER; ++e0) {
-      const int e = tid + NTH * e0, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
-      if (PIECES % NTH == 0 || e < PIECES) {
-        *reinterpret_cast<u32x4_t*>(&sK[row * kColLd<DK> + cc]) = bf16x8_as_f16(gk[e0]);
-        *reinterpret_cast<u32x4_t*>(&sQ[row * kColLd<DK> + cc]) = bf16x8_as_f16(gq[e0]);
-      }
-    }
-    stage_bwd_img<NTH, IPER>(sImg, gi);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) *reinterpret_cast<u32x2_t*>(&sT[w][(16 * t + lr) * 16 + 4 * lq]) = BACK ? gd[t] : gv[t];
-    u32x2_t oth[4];  // forward: dY, channels 4 lq .. + 3 of token 16 t + lr
-#pragma unroll
-    for (int t = 0; t < 4; ++t) oth[t] = gd[t];
-    f16x8_t s0[BACK ? 2 * KT : 1], r0[BACK ? 4 : 1];
-    if constexpr (BACK) {
-#pragma unroll
-      for (int e = 0; e < 2 * KT; ++e) s0[e] = gs[e];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r0[e] = gr[e];
-    }
-    __syncthreads();
-    load(BACK ? c - 1 : c + 1);
-
-    u32x2_t tq[4];  // this wavefront's V (dY): tokens 16 t + 4 lq .. + 3 of channel lr
-#pragma unroll
-    for (int t = 0; t < 4; ++t) tq[t] = lds_tr4(&sT[w][(16 * t + 4 * lq + (lr >> 2)) * 16 + 4 * (lr & 3)]);
+    const Lds& b = lds[i & 1];
+    Lds& next = lds[(i + 1) & 1];
+    auto img_frag = [&](int f) { return *reinterpret_cast<const f16x8_t*>(&b.img[f * kFrag + lane * 16]); };
+    auto gate = [&](int which, int t) {
+      return *reinterpret_cast<const f32x4_t*>(&b.img[GATES + which * 256 + (16 * t + 4 * lq) * 4]);
+    };
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float fade = bwd_gate1(sImg, kBwdGrow, kDeltaC - 1);
-    // K times the (adjoint) state, 64 x 16; back, K times S0 beside it
-    f32x4_t x[4], z[BACK ? 4 : 1];
+    constexpr int STEPS = 4 * KT;
+    auto tile_of = [](int j) { return (j / KT + 2) & 3; };  // tokens' tiles in the order 2, 3, 0, 1: T^T takes the last two first
+    f16x8_t kf[4];
+    auto read_step = [&](int j) { kf[j & 3] = plain_row_frag<CL>(b.k, 16 * tile_of(j) + lr, j % KT, lq); };
+    u32x2_t tq[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      x[t] = zero;
-      if constexpr (BACK) z[t] = zero;
+    for (int t = 0; t < 4; ++t) tq[t] = lds_tr4(&lds_y[w][(16 * t + 4 * lq + (lr >> 2)) * 16 + 4 * (lr & 3)]);
+    f32x4_t outg[4];
 #pragma unroll
-      for (int kk = 0; kk < KT; ++kk) {
-        const f16x8_t kf = plain_row_frag<kColLd<DK>>(sK, 16 * t + lr, kk, lq);
-        x[t] = mfma_f16(kf, Sl[kk], x[t]);
-        if constexpr (BACK) z[t] = mfma_f16(kf, s0[KT + kk], z[t]);
-        x[t] = mfma_f16(kf, Sh[kk], x[t]);
-        if constexpr (BACK) z[t] = mfma_f16(kf, s0[kk], z[t]);
-      }
-    }
-    const int64_t mytile = cell * bp.tiles + tile;
-    if constexpr (!BACK) {
-      char* keep = bp.state + mytile * (2 * KT * kFrag) + lane * 16;
-      if (mine) {
+    for (int t = 0; t < 4; ++t) outg[t] = gate(1, t);
+    const float fade = *reinterpret_cast<const float*>(&b.img[GATES + (kDeltaC - 1) * 4]);
+    f16x8_t pf[6];
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-          *reinterpret_cast<f16x8_t*>(keep + kk * kFrag) = Sh[kk];
-          *reinterpret_cast<f16x8_t*>(keep + (KT + kk) * kFrag) = Sl[kk];
-        }
-      }
-      // (S0 q) . dy of each token over these 16 channels, and the largest |dy|
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        f32x4_t o = zero;
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-          const f16x8_t qf = plain_row_frag<kColLd<DK>>(sQ, 16 * t + lr, kk, lq);
-          o = mfma_f16(Sl[kk], qf, o);
-          o = mfma_f16(Sh[kk], qf, o);
-        }
-        const f32x4_t d = bf16x4_f32(oth[t], 1.0f);
-        float s = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          s = __builtin_fmaf(o[r], d[r], s);
-          amax = __builtin_fmaxf(amax, __builtin_fabsf(d[r]));
-        }
-        s = sum_groups(s) * bwd_gate1(sImg, kBwdOut, 16 * t + lr);
-        if (mine && lq == 0) bp.oterm[mytile * kDeltaC + 16 * t + lr] = s;
-        const f32x4_t grow = bwd_gate(sImg, kBwdGrow, t, lq), v = bf16x4_f32(tq[t], 1.0f);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(-grow[r], x[t][r], v[r]);
-      }
-      // R = T X, kept as a pair
-      f16x8_t Xh[2], Xl[2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) split_f16(x[2 * m], x[2 * m + 1], Xh[m], Xl[m]);
-      f32x4_t u[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        u[t] = zero;
-#pragma unroll
-        for (int m = 0; m <= t / 2; ++m) {
-          const f16x8_t th = bwd_row_frag(sImg, frag_of(t, m), lr, lq);
-          const f16x8_t tl = bwd_row_frag(sImg, 6 + frag_of(t, m), lr, lq);
-          u[t] = mfma_f16(th, Xh[m], u[t]);
-          u[t] = mfma_f16(th, Xl[m], u[t]);
-          u[t] = mfma_f16(tl, Xh[m], u[t]);
-        }
-      }
-      char* kr = bp.r + mytile * (4 * kFrag) + lane * 16;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        f16x8_t Rh, Rl;
-        split_f16(u[2 * m], u[2 * m + 1], Rh, Rl);
-        if (mine) {
-          *reinterpret_cast<f16x8_t*>(kr + m * kFrag) = Rh;
-          *reinterpret_cast<f16x8_t*>(kr + (2 + m) * kFrag) = Rl;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) u[t] *= bwd_gate(sImg, kBwdBeta, t, lq);  // U
-      // S = e^{cs_C} S + K^T diag(L) U
-#pragma unroll
-      for (int d = 0; d < DT; ++d) S[d] *= fade;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        f16x8_t Uh, Ul;
-        split_f16(u[2 * m] * bwd_gate(sImg, kBwdLeft, 2 * m, lq), u[2 * m + 1] * bwd_gate(sImg, kBwdLeft, 2 * m + 1, lq),
-                  Uh, Ul);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const f16x8_t kc = lds_col_frag<DK>(sK, 32 * m, d, lr, lq);
-          S[d] = mfma_f16(kc, Uh, S[d]);
-          S[d] = mfma_f16(kc, Ul, S[d]);
-        }
-      }
-    } else {
-      char* keep = bp.adj + mytile * (KT * kFrag) + lane * 16;
-      if (mine) {
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) *reinterpret_cast<f16x8_t*>(keep + kk * kFrag) = Sh[kk];
-      }
-      // e^{cs_C} <dS, S0>
-      {
-        float s = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const f16x8_t hi = s0[kk], lo = s0[KT + kk];
-            s = __builtin_fmaf(S[2 * kk][r], static_cast<float>(hi[r]) + static_cast<float>(lo[r]), s);
-            s = __builtin_fmaf(S[2 * kk + 1][r], static_cast<float>(hi[4 + r]) + static_cast<float>(lo[4 + r]), s);
-          }
-        s = sum_wave(s);
-        if (lane == 0 && mine) bp.edge[mytile] = s * fade * inv;
-      }
-      // diag(b) Y0 = diag(b) (diag(L) K dS + P0^T dY); on the way L (K dS) . u of each token
+    for (int f = 0; f < 6; ++f) pf[f] = img_frag(18 + f);
+    __builtin_amdgcn_sched_barrier(0);
+    next_rsrc(i + 2 < nchunks);
+    ro = os.take(i > 0);  // of the chunk before this one in the walk
+    rs0 = ss.take(i + 1 < nchunks), rr0 = rs.take(i + 1 < nchunks);
+    const rsrc_t ra = as.take(true);
+    constexpr int SLOTS = STEPS + 2 * KT;
+    auto slot = [&](auto place) {
+      constexpr int k = decltype(place)::value, i0 = k * ITEMS / SLOTS, i1 = (k + 1) * ITEMS / SLOTS;
+      static_for<i1 - i0>([&](auto n) {
+        stage_item(next, IC<i0 + decltype(n)::value>{});
+        load_item(IC<i0 + decltype(n)::value>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // ---- P0^T dY (16 times as large), and dY's operands (Df is exact: bf16 values scaled by a power of two)
+    f32x4_t wy[4];
+    f16x8_t Gh[2], Gl[2], Df[2];
+    {
       f32x4_t d[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        d[t] = bf16x4_f32(tq[t], sc);
-        x[t] *= bwd_gate(sImg, kBwdLeft, t, lq);
-        const f32x4_t beta = bwd_gate(sImg, kBwdBeta, t, lq);
-        f32x4_t l;
+      for (int t = 0; t < 4; ++t) d[t] = bf16x4_f32(tq[t], sc), wy[t] = zero;
+      Df[0] = pair_f16(d[0], d[1]), Df[1] = pair_f16(d[2], d[3]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int e = 4 * (t & 1) + r;
-          l[r] = x[t][r] * (static_cast<float>(r0[t >> 1][e]) + static_cast<float>(r0[2 + (t >> 1)][e])) * beta[r];
-        }
-        x[t] *= kBwdPScale;
-        l = sum_lanes16(l);
-        if (mine && lr == 0) *reinterpret_cast<f32x4_t*>(&bp.lterm[mytile * kDeltaC + 16 * t + 4 * lq]) = l * inv;
-      }
-      const f16x8_t Df[2] = {pair_f16(d[0], d[1]), pair_f16(d[2], d[3])};  // exact: bf16 values scaled by a power of 2
+      for (int part = 0; part < 2; ++part) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+        for (int m = 1; m >= 0; --m)
 #pragma unroll
-        for (int m = t / 2; m < 2; ++m) {
-          x[t] = mfma_f16(bwd_col_frag(sImg, 12, t, m, lr, lq), Df[m], x[t]);
-          x[t] = mfma_f16(bwd_col_frag(sImg, 18, t, m, lr, lq), Df[m], x[t]);
-        }
-        x[t] *= bwd_gate(sImg, kBwdBeta, t, lq) * (1.0f / kBwdPScale);
-      }
-      // dV = T^T diag(b) Y0, kept as a pair; its transpose (rows of channels, from the hi parts) to store as bf16
-      f16x8_t Zh[2], Zl[2];
+          for (int t = 0; t < 2 + 2 * m; ++t) wy[t] = mfma_f16(pf[back_frag(t, m)], Df[m], wy[t]);
+        if (part == 0) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) split_f16(x[2 * m], x[2 * m + 1], Zh[m], Zl[m]);
-      f32x4_t u[4];
-      const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(bp.dv) + tok * rowe + h * p.P, ((nt - 1) * rowe + p.P) * 2);
+          for (int f = 0; f < 6; ++f) pf[f] = img_frag(12 + f);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        u[t] = zero;
-        f32x4_t vt = zero;
+          for (int j = 0; j < 3; ++j) read_step(j);
 #pragma unroll
-        for (int m = t / 2; m < 2; ++m) {
-          const f16x8_t th = bwd_col_frag(sImg, 0, t, m, lr, lq), tl = bwd_col_frag(sImg, 6, t, m, lr, lq);
-          u[t] = mfma_f16(th, Zh[m], u[t]);
-          u[t] = mfma_f16(th, Zl[m], u[t]);
-          u[t] = mfma_f16(tl, Zh[m], u[t]);
-          vt = mfma_f16(Zh[m], th, vt);
-        }
-        vt *= inv;
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{pack_bf16x2(vt[0], vt[1]), pack_bf16x2(vt[2], vt[3])}, ro,
-                                              yrow + ctile, 32 * t * rowe32, 0);
-        // e^cs (S0 k) . dv of each token
-        const f32x4_t grow = bwd_gate(sImg, kBwdGrow, t, lq);
-        const f32x4_t gt = sum_lanes16(u[t] * z[t] * grow);
-        if (mine && lr == 0) *reinterpret_cast<f32x4_t*>(&bp.gterm[mytile * kDeltaC + 16 * t + 4 * lq]) = gt * inv;
-      }
-      char* kv = bp.dvh + mytile * (4 * kFrag) + lane * 16;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        f16x8_t Vh, Vl;
-        split_f16(u[2 * m], u[2 * m + 1], Vh, Vl);
-        if (mine) {
-          *reinterpret_cast<f16x8_t*>(kv + m * kFrag) = Vh;
-          *reinterpret_cast<f16x8_t*>(kv + (2 + m) * kFrag) = Vl;
-        }
-      }
-      // dS = e^{cs_C} dS + Q^T diag(scale e^cs) dY - K^T diag(e^cs) dV
-#pragma unroll
-      for (int e = 0; e < DT; ++e) S[e] *= fade;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        f16x8_t Gh, Gl, Vh, Vl;
-        split_f16(d[2 * m] * bwd_gate(sImg, kBwdOut, 2 * m, lq), d[2 * m + 1] * bwd_gate(sImg, kBwdOut, 2 * m + 1, lq),
-                  Gh, Gl);
-        split_f16(u[2 * m] * -bwd_gate(sImg, kBwdGrow, 2 * m, lq),
-                  u[2 * m + 1] * -bwd_gate(sImg, kBwdGrow, 2 * m + 1, lq), Vh, Vl);
-#pragma unroll
-        for (int e = 0; e < DT; ++e) {
-          const f16x8_t qc = lds_col_frag<DK>(sQ, 32 * m, e, lr, lq), kc = lds_col_frag<DK>(sK, 32 * m, e, lr, lq);
-          S[e] = mfma_f16(qc, Gh, S[e]);
-          S[e] = mfma_f16(qc, Gl, S[e]);
-          S[e] = mfma_f16(kc, Vh, S[e]);
-          S[e] = mfma_f16(kc, Vl, S[e]);
+          for (int m = 0; m < 2; ++m) split_f16(d[2 * m] * outg[2 * m], d[2 * m + 1] * outg[2 * m + 1], Gh[m], Gl[m]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
+    // ---- K dS, and K S0 and <dS, S0> beside it
+    f32x4_t x[4], z[4], e0 = zero, e1 = zero, lt[4], left, beta;
+    f16x8_t Zh[2], Zl[2], tf[12];
+    // b Y0 of a tile, and on the way L (K dS) . u of its tokens
+    auto finish = [&](int t) {
+      const int m = t >> 1;
+      const f32x4_t lx = x[t] * left;
+      const f16x8_t hi = r0[m], lo = r0[2 + m];
+      const f16x4_t hs = t & 1 ? __builtin_shufflevector(hi, hi, 4, 5, 6, 7) : __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
+      const f16x4_t ls4 = t & 1 ? __builtin_shufflevector(lo, lo, 4, 5, 6, 7) : __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
+      lt[t] = fma_pair(lx * beta, hs, ls4, zero);
 #pragma unroll
-    for (int kk = 0; kk < KT; ++kk) split_f16(S[2 * kk], S[2 * kk + 1], Sh[kk], Sl[kk]);
+      for (int r = 0; r < 4; ++r) x[t][r] = beta[r] * __builtin_fmaf(wy[t][r], 1.0f / kBwdPScale, lx[r]);
+      if (t & 1) {
+        split_f16(x[t - 1], x[t], Zh[m], Zl[m]);
+        load_r(m);
+      }
+    };
+    static_for<STEPS>([&](auto step) {
+      constexpr int j = decltype(step)::value, kk = j % KT;
+      const int t = tile_of(j);
+      if constexpr (j + 3 < STEPS)
+        read_step(j + 3);
+      else {  // T^T's fragments of tokens 32 .. 63
+        tf[j + 3 - STEPS] = img_frag(back_frag(j + 3 - STEPS, 1));
+        tf[6 + j + 3 - STEPS] = img_frag(6 + back_frag(j + 3 - STEPS, 1));
+      }
+      if (kk == KT - 1) left = gate(2, t), beta = gate(3, t);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kk == 0) x[t] = z[t] = zero;
+      x[t] = mfma_f16(kf[j & 3], Sl[kk], x[t]);
+      z[t] = mfma_f16(kf[j & 3], s0[KT + kk], z[t]);
+      x[t] = mfma_f16(kf[j & 3], Sh[kk], x[t]);
+      z[t] = mfma_f16(kf[j & 3], s0[kk], z[t]);
+      if constexpr (j / KT == 0) {
+        e0 = mfma_f16(Sl[kk], s0[kk], e0);
+        e1 = mfma_f16(Sh[kk], s0[kk], e1);
+        e0 = mfma_f16(Sh[kk], s0[KT + kk], e0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Sh[kk]), ra, mine, kk * kFrag, 0);
+      }
+      if constexpr (j / KT == 3) load_s0(kk);
+      if constexpr (kk == KT - 1 && j + 1 < STEPS) finish(t);
+#pragma unroll
+      for (int d = j * DT / STEPS; d < (j + 1) * DT / STEPS; ++d) S[d] *= fade;
+      slot(IC<j>{});
+    });
+    // ---- dV = T^T (b Y0): the last two tiles' share of it while the rest of b Y0 is finished, Q^T dY between
+    f32x4_t u[4], vt[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) u[t] = vt[t] = zero;
+    tf[3] = img_frag(back_frag(3, 1)), tf[9] = img_frag(6 + back_frag(3, 1));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) tf[4 + t] = img_frag(back_frag(t, 0)), tf[10 + t] = img_frag(6 + back_frag(t, 0));
+    f16x8_t cf[DT];  // columns of Q, then of K
+#pragma unroll
+    for (int d = 0; d < DT; ++d) cf[d] = lds_col_frag<DK>(b.q, 0, d, lr, lq);
+    f32x4_t grow[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) grow[t] = gate(0, t);
+    __builtin_amdgcn_sched_barrier(0);
+    auto t_products = [&](int t, int m) {
+      const int f = m ? t : 4 + t;
+      u[t] = mfma_f16(tf[f], Zh[m], u[t]);
+      vt[t] = mfma_f16(Zh[m], tf[f], vt[t]);
+      u[t] = mfma_f16(tf[f], Zl[m], u[t]);
+      u[t] = mfma_f16(tf[6 + f], Zh[m], u[t]);
+    };
+    t_products(2, 1);
+    t_products(3, 1);
+    finish(tile_of(STEPS - 1));
+    t_products(0, 1);
+    t_products(1, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    auto state_product = [&](int d, const f16x8_t& hi, const f16x8_t& lo) {
+      S[d] = mfma_f16(cf[d], hi, S[d]);
+      S[d + 1] = mfma_f16(cf[d + 1], hi, S[d + 1]);
+      S[d] = mfma_f16(cf[d], lo, S[d]);
+      S[d + 1] = mfma_f16(cf[d + 1], lo, S[d + 1]);
+    };
+    static_for<KT>([&](auto k) {
+      constexpr int d = 2 * decltype(k)::value;
+      state_product(d, Gh[0], Gl[0]);
+      cf[d] = lds_col_frag<DK>(b.q, 32, d, lr, lq);
+      cf[d + 1] = lds_col_frag<DK>(b.q, 32, d + 1, lr, lq);
+    });
+    t_products(0, 0);
+    t_products(1, 0);
+    f16x8_t Vh[2], Vl[2], Nh, Nl;
+    const rsrc_t rv = vs.take(true);
+    f32x4_t gt[4];
+    // dV of two tiles: kept as a pair, times -e^cs as the next product's operand; e^cs (S0 k) . dv of its tokens
+    auto take_dv = [&](int m) {
+      split_f16(u[2 * m], u[2 * m + 1], Nh, Nl);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Nh), rv, mine, m * kFrag, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Nl), rv, mine, (2 + m) * kFrag, 0);
+      const f32x4_t v0 = u[2 * m] * -grow[2 * m], v1 = u[2 * m + 1] * -grow[2 * m + 1];
+      split_f16(v0, v1, Vh[m], Vl[m]);
+      gt[2 * m] = v0 * z[2 * m], gt[2 * m + 1] = v1 * z[2 * m + 1];
+    };
+    take_dv(1);
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<KT>([&](auto k) {
+      constexpr int d = 2 * decltype(k)::value;
+      state_product(d, Gh[1], Gl[1]);
+      cf[d] = lds_col_frag<DK>(b.k, 32, d, lr, lq);
+      cf[d + 1] = lds_col_frag<DK>(b.k, 32, d + 1, lr, lq);
+      slot(IC<STEPS + decltype(k)::value>{});
+    });
+    take_dv(0);
+    // ---- dS = e^{cs_C} dS + Q^T diag(scale e^cs) dY - K^T diag(e^cs) dV
+    static_for<KT>([&](auto k) {
+      constexpr int d = 2 * decltype(k)::value;
+      state_product(d, Vh[1], Vl[1]);
+      cf[d] = lds_col_frag<DK>(b.k, 0, d, lr, lq);
+      cf[d + 1] = lds_col_frag<DK>(b.k, 0, d + 1, lr, lq);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<KT>([&](auto k) {
+      constexpr int kk = decltype(k)::value, d = 2 * kk;
+      state_product(d, Vh[0], Vl[0]);
+      if constexpr (kk > 0) split_f16(S[d - 2], S[d - 1], Sh[kk - 1], Sl[kk - 1]);
+      slot(IC<STEPS + KT + kk>{});
+    });
+    // ---- the terms of dla, and dV's rows
+    rsrc_t rt = ls.take(true);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(lt, lr) * inv), rt, term_at, 0, 0);
+    rt = gs.take(true);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(gt, lr) * -inv), rt, term_at, 0, 0);
+    e0 += e1;  // its diagonal: each channel's <dS, S0>
+    const float diag = (lr & 2) ? ((lr & 1) ? e0[3] : e0[2]) : ((lr & 1) ? e0[1] : e0[0]);
+    rt = es.take(true);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lq == (lr >> 2) ? diag * fade * inv : 0.0f), rt, mine4, 0, 0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      vt[t] *= inv;
+      yo[t] = u32x2_t{pack_bf16x2(vt[t][0], vt[t][1]), pack_bf16x2(vt[t][2], vt[t][3])};
+    }
+    split_f16(S[DT - 2], S[DT - 1], Sh[KT - 1], Sl[KT - 1]);
+    __syncthreads();
   }
-  if constexpr (!BACK) {
-    // the largest magnitude of the unit's dY and dfinal
-    if (nchunks > 0 && mine) {
-      if (bp.dfinal) {
+  if (nchunks > 0) {
+    ro = os.take(true);
+    static_for<2>([&](auto n) { stage_item(lds[0], IC<LOADS + decltype(n)::value>{}); });
+  }
+  if (bp.dh0 && has) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const f32x4_t f = *reinterpret_cast<const f32x4_t*>(bp.dfinal + sbase + 16 * d);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[r]));
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 64));
-      // a maximum does not depend on the order of its arguments, so neither does the scale
-      if (lane == 0 && p.amax) atomicMax(p.amax + unit, __float_as_uint(amax));
-    }
-  } else {
-    if (bp.dh0 && mine) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4_t*>(bp.dh0 + sbase + 16 * d) = S[d] * inv;
-    }
+    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4_t*>(bp.dh0 + sbase + 16 * d) = S[d] * inv;
   }
 }
 
@@ -481,6 +479,12 @@ template <int LD> __device__ __forceinline__ f16x8_t tok_frag(const uint16_t* ba
   const uint16_t* a = base + (4 * lq + (lr >> 2)) * LD + 16 * t + 4 * (lr & 3);
   const u32x2_t x = lds_tr4(a), y = lds_tr4(a + 16 * LD);
   return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
+}
+
+__device__ __forceinline__ float sum_wave(float v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+  return v;
 }
 
 template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(DeltaBwdParams bp) {
@@ -599,7 +603,7 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
       const int64_t at = (cell * bp.tiles + t) * kDeltaC + lane;
       og += static_cast<double>(bp.oterm[at]) - static_cast<double>(bp.gterm[at]);
       lt += bp.lterm[at];
-      edge += bp.edge[cell * bp.tiles + t];
+      edge += bp.edge[at];
     }
     for (int b = 0; b < nb; ++b) {
       __syncthreads();  // the last block (or head) is read
@@ -743,6 +747,8 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
       if (part == 0) lds.e[t] = e;
       lds.og[w][lane] = og;
       lds.l[w][lane] = lt;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) edge += __shfl_xor(edge, o, 64);
       if (lane == 0) lds.edge[w] = edge;
     }
     __syncthreads();

@@ -49,10 +49,11 @@ constexpr int kImgGrow = 18 * kFrag;         // e^{cs_t}
 constexpr int kImgOut = kImgGrow + 256;      // scale e^{cs_t}
 constexpr int kImgLeft = kImgGrow + 512;     // e^{cs_C - cs_t} b_t (0 behind the sequence's end)
 constexpr int kImgBytes = kImgGrow + 768;
-// The backward's image: the same fragments of T, then P without b as a pair, and the gates.
+// The backward's image: the same fragments of T (for its walk forward), then T's and P's transposes (for its walk back;
+// P without b), each a pair, and the gates.
 constexpr float kBwdPScale = 16.0f;          // P is kept 16 times as large, away from the last places of fp16
-constexpr int kBwdPlo = 18 * kFrag;
-constexpr int kBwdGates = 24 * kFrag;
+constexpr int kBwdBack = 12 * kFrag;         // T^T hi, T^T lo, P^T hi, P^T lo: six fragments each
+constexpr int kBwdGates = kBwdBack + 24 * kFrag;
 constexpr int kBwdGrow = kBwdGates;          // e^{cs_t}
 constexpr int kBwdOut = kBwdGates + 256;     // scale e^{cs_t}
 constexpr int kBwdLeft = kBwdGates + 512;    // e^{cs_C - cs_t}
@@ -60,6 +61,8 @@ constexpr int kBwdBeta = kBwdGates + 768;    // b_t
 constexpr int kBwdCs = kBwdGates + 1024;     // cs_t, as a pair of floats: hi, then lo
 constexpr int kBwdImgBytes = kBwdGates + 1536;
 __host__ __device__ constexpr int frag_of(int t, int m) { return t < 2 ? t : 2 + 2 * (t - 2) + m; }
+// The same of the transposes, upper triangular: row tile t, column pair m >= t / 2.
+__host__ __device__ constexpr int back_frag(int t, int m) { return m ? t : 4 + t; }
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
@@ -229,7 +232,7 @@ struct DeltaBwdParams {
   float* oterm;
   float* gterm;
   float* lterm;
-  float* edge;          // [slots][H][tiles]: e^{cs_C} <dS, S0>
+  float* edge;          // [slots][H][tiles][64]: parts of e^{cs_C} <dS, S0>
   float* part;          // [slots][H][2]: parts of dA and dbias
   int64_t tiles;        // P / 16
 };

@@ -167,8 +167,35 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
       m[jt][r] = j < t ? sBeta[j] * fade(t, j) * m[jt][r] : 0.0f;
     }
   }
-  // ---- P: the tiles of K Q^T leave four consecutive j of token t = lr in a lane, half a fragment
-  {
+  // ---- P^T: the tiles of Q K^T leave four consecutive t of token j = lr in a lane, half a fragment
+  if constexpr (BWD) {
+    const int j = 16 * w + lr;
+    for (int m2 = w / 2; m2 < 2; ++m2) {
+      f32x4_t half[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tt = 2 * m2 + u;
+        f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (tt >= w) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 32; ++kk)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sQ, tt, kk), frag(sK, w, kk), acc, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = 16 * tt + 4 * lq + r;
+            acc[r] = j <= t ? p.scale * kBwdPScale * fade(t, j) * acc[r] : 0.0f;
+          }
+        }
+        half[u] = acc;
+      }
+      f16x8_t hi, lo;
+      split_f16(half[0], half[1], hi, lo);
+      char* out = p.img + id * IMG + kBwdBack + (12 + back_frag(w, m2)) * kFrag + lane * 16;
+      *reinterpret_cast<f16x8_t*>(out) = hi;
+      *reinterpret_cast<f16x8_t*>(out + 6 * kFrag) = lo;
+    }
+  } else {
+    // ---- P: the tiles of K Q^T leave four consecutive j of token t = lr in a lane, half a fragment
     const int tt = 3 - w, t = 16 * tt + lr;
     for (int m2 = 0; m2 <= tt / 2; ++m2) {
       f32x4_t half[2];
@@ -183,21 +210,14 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * jt + 4 * lq + r;
-            acc[r] = j <= t ? p.scale * (BWD ? kBwdPScale : sBeta[j]) * fade(t, j) * acc[r] : 0.0f;
+            acc[r] = j <= t ? p.scale * sBeta[j] * fade(t, j) * acc[r] : 0.0f;
           }
         }
         half[u] = acc;
       }
-      char* out = p.img + id * IMG + kImgP + frag_of(tt, m2) * kFrag + lane * 16;
-      if constexpr (BWD) {
-        f16x8_t hi, lo;
-        split_f16(half[0], half[1], hi, lo);
-        *reinterpret_cast<f16x8_t*>(out) = hi;
-        *reinterpret_cast<f16x8_t*>(out + kBwdPlo - kImgP) = lo;
-      } else {
-        // fp16: P meets R (fp16 too) in y alone, which is stored with 8 significant bits
-        *reinterpret_cast<f16x8_t*>(out) = pair_f16(half[0], half[1]);
-      }
+      // fp16: P meets R (fp16 too) in y alone, which is stored with 8 significant bits
+      *reinterpret_cast<f16x8_t*>(p.img + id * IMG + kImgP + frag_of(tt, m2) * kFrag + lane * 16) =
+          pair_f16(half[0], half[1]);
     }
   }
   __syncthreads();  // K and Q are read
@@ -251,6 +271,25 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
     char* out = p.img + id * IMG + f * kFrag + ln * 16;
     *reinterpret_cast<f16x8_t*>(out + kImgThi) = hi;
     *reinterpret_cast<f16x8_t*>(out + kImgTlo) = lo;
+  }
+  if constexpr (BWD) {
+    // ---- and its transpose's: token j = 16 (row tile) + row, four consecutive t twice
+    for (int e = tid; e < 6 * 64; e += 256) {
+      const int f = e >> 6, ln = e & 63, row = ln & 15, q4 = 4 * (ln >> 4);
+      const int j = f < 4 ? f : f - 4, m = f < 4 ? 1 : 0;
+      f32x4_t half[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = 2 * m + u;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) half[u][r] = t < j ? 0.0f : sM[(16 * j + q4 + r) * kPrepLd + 16 * t + row];
+      }
+      f16x8_t hi, lo;
+      split_f16(half[0], half[1], hi, lo);
+      char* out = p.img + id * IMG + kBwdBack + f * kFrag + ln * 16;
+      *reinterpret_cast<f16x8_t*>(out) = hi;
+      *reinterpret_cast<f16x8_t*>(out + 6 * kFrag) = lo;
+    }
   }
 }
 

@@ -41,7 +41,7 @@ BwdLayout bwd_layout(int64_t rows, int64_t slots, int64_t heads, int64_t headdim
   l.oterm = take(cells * tiles * kDeltaC * 4);
   l.gterm = take(cells * tiles * kDeltaC * 4);
   l.lterm = take(cells * tiles * kDeltaC * 4);
-  l.edge = take(cells * tiles * 4);
+  l.edge = take(cells * tiles * kDeltaC * 4);
   l.part = take(cells * 2 * 4);
   l.total = at;
   return l;
@@ -63,7 +63,7 @@ template <int DK> hipError_t run_bwd(const DeltaBwdParams& bp, hipStream_t s) {
     hipLaunchKernelGGL((delta_walk_kernel<DK, 4, true>), dim3(walks), dim3(256), 0, s, bp);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((delta_bwd_walk_kernel<DK, W, true>), dim3(walks), dim3(64 * W), 0, s, bp);
+  hipLaunchKernelGGL((delta_bwd_walk_kernel<DK, W>), dim3(walks), dim3(64 * W), 0, s, bp);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((delta_grad_kernel<DK>), dim3(static_cast<unsigned>(p.slots * p.G)), dim3(256), 0, s, bp);
