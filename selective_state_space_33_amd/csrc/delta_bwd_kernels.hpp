@@ -125,9 +125,9 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t blocks = (p.P + 16 * W - 1) / (16 * W);
-  const int64_t id = xcd_order(blockIdx.x, p.rows * p.H * blocks);
-  const int64_t unit = id / blocks, seq = unit / p.H, h = unit % p.H, g = h / (p.H / p.G);
-  const int col = static_cast<int>((id % blocks) * W + w) * 16;
+  const DeltaUnit un = delta_unit(p, blocks);
+  const int64_t seq = un.seq, h = un.h, unit = seq * p.H + h, g = h / (p.H / p.G);
+  const int col = static_cast<int>(un.block * W + w) * 16;
   const DeltaSeq sq = delta_seq(p.cu, seq, p.L, p.chunks);
   const int nchunks = static_cast<int>((sq.len + kDeltaC - 1) / kDeltaC);
   const int64_t rowe = p.H * p.P, krow = p.G * DK;
@@ -498,14 +498,7 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
   const int64_t slot = id / p.G, g = id % p.G, rep = p.H / p.G;
   int64_t s = 0;
   if (p.cu) {
-    int64_t hi = p.rows - 1;
-    while (s < hi) {
-      const int64_t mid = (s + hi + 1) / 2;
-      if (delta_seq(p.cu, mid, p.L, 0).slot <= slot)
-        s = mid;
-      else
-        hi = mid - 1;
-    }
+    s = delta_slot_seq(p.cu, p.rows, p.L, slot);
   } else {
     s = slot / p.chunks;
   }

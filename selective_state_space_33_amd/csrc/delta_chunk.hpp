@@ -175,6 +175,20 @@ __device__ __forceinline__ DeltaSeq delta_seq(const int64_t* cu, int64_t s, int6
   return d;
 }
 
+// The last sequence of n that starts at or before a chunk slot, by a whole wavefront: 64 places are tried at once.
+__device__ __forceinline__ int64_t delta_slot_seq(const int64_t* cu, int64_t n, int64_t L, int64_t slot) {
+  const int64_t lane = threadIdx.x & 63;
+  int64_t lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step;
+    const bool before = at <= hi && delta_seq(cu, at, L, 0).slot <= slot;
+    const int64_t count = __popcll(__ballot(before));  // (the slots ascend)
+    lo += count * step;
+    hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+  }
+  return lo;
+}
+
 // A channel tile that the head does not have is addressed here: behind every
 // resource (they are cut to this length, and a chunk's offsets, 64 rows of at
 // most 2^23 bytes, stay below half of it), so loads return zero and stores are
@@ -188,6 +202,18 @@ __device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
   return x * q + (x < r ? x : r) + i / 8;
 }
 
+// The (sequence, head) unit and block of channels of a walk's workgroup.  Rows of one length go to the XCDs in runs;
+// packed sequences are handed out longest first over all of them (in runs, one XCD gets all the heads of the longest
+// sequence), so that the last ones are short.
+struct DeltaUnit {
+  int64_t seq, h, block;
+};
+template <class P> __device__ __forceinline__ DeltaUnit delta_unit(const P& p, int64_t blocks) {
+  const int64_t id = p.cu ? static_cast<int64_t>(blockIdx.x) : xcd_order(blockIdx.x, p.rows * p.H * blocks);
+  const int64_t unit = id / blocks, s = unit / p.H;
+  return {p.cu ? static_cast<int64_t>(p.order[s]) : s, unit % p.H, id % blocks};
+}
+
 struct DeltaChunkParams {
   const void* q;       // [tokens][G][N] bf16
   const void* k;
@@ -199,6 +225,7 @@ struct DeltaChunkParams {
   const float* h0;     // [rows][H][P][N] (nullable); may be hT
   float* hT;           // (nullable)
   const int64_t* cu;   // (nullable)
+  int* order;          // with cu: the sequences, longest first
   void* y;
   char* img;           // [slots][H][kImgBytes]
   unsigned* words;     // workspace header

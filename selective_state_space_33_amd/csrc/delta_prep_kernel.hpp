@@ -67,14 +67,7 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
   // the sequence of this slot: the last one that starts at or before it
   int64_t s = 0;
   if (p.cu) {
-    int64_t hi = p.rows - 1;
-    while (s < hi) {
-      const int64_t mid = (s + hi + 1) / 2;
-      if (delta_seq(p.cu, mid, p.L, 0).slot <= slot)
-        s = mid;
-      else
-        hi = mid - 1;
-    }
+    s = delta_slot_seq(p.cu, p.rows, p.L, slot);
   } else {
     s = slot / p.chunks;
   }

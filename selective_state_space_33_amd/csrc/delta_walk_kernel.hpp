@@ -82,9 +82,9 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t blocks = (p.P + 16 * W - 1) / (16 * W);  // workgroups per unit
-  const int64_t id = xcd_order(blockIdx.x, p.rows * p.H * blocks);
-  const int64_t unit = id / blocks, seq = unit / p.H, h = unit % p.H, g = h / (p.H / p.G);
-  const int col = static_cast<int>((id % blocks) * W + w) * 16;  // first channel of this wavefront
+  const DeltaUnit un = delta_unit(p, blocks);
+  const int64_t seq = un.seq, h = un.h, unit = seq * p.H + h, g = h / (p.H / p.G);
+  const int col = static_cast<int>(un.block * W + w) * 16;  // first channel of this wavefront
   const DeltaSeq sq = delta_seq(p.cu, seq, p.L, p.chunks);
   const int nchunks = static_cast<int>((sq.len + kDeltaC - 1) / kDeltaC);
   const int64_t rowe = p.H * p.P, krow = p.G * DK;

@@ -9,6 +9,7 @@
 #include "delta_step_kernel.hpp"
 #include "delta_walk_kernel.hpp"
 #include "host_common.hpp"
+#include "order_kernel.hpp"
 #include "ssm_scan.h"
 
 namespace ssm {
@@ -125,7 +126,7 @@ extern "C" size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t
   if ((nseq > 0 && batch != 1) || nseq < 0) return 0;
   if (!delta_shape_supported(nseq > 0 ? nseq : batch, L, heads, headdim, dstate)) return 0;
   if (!delta_chunked(L, heads, headdim, dstate, nseq, dt)) return 0;
-  return kDeltaHeader + static_cast<size_t>(delta_slots(batch, L, nseq)) * heads * kImgBytes;
+  return kDeltaHeader + delta_order_bytes(nseq) + static_cast<size_t>(delta_slots(batch, L, nseq)) * heads * kImgBytes;
 }
 
 extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
@@ -164,7 +165,8 @@ extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* 
   p.cu = cu_seqlens;
   p.y = y;
   p.words = static_cast<unsigned*>(workspace);
-  p.img = static_cast<char*>(workspace) + kDeltaHeader;
+  p.order = reinterpret_cast<int*>(static_cast<char*>(workspace) + kDeltaHeader);
+  p.img = static_cast<char*>(workspace) + kDeltaHeader + delta_order_bytes(cu_seqlens ? nseq : 0);
   p.rows = cu_seqlens ? nseq : batch;
   p.L = L;
   p.H = heads;
@@ -175,6 +177,11 @@ extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* 
   p.softplus = a.softplus;
   p.sigmoid = a.sigmoid;
   p.scale = scale;
+  if (cu_seqlens) {
+    hipLaunchKernelGGL(packed_order_kernel, dim3(1), dim3(kOrderBins), 0, stream, p.cu, static_cast<int>(nseq), L,
+                       p.order);
+    if (hipGetLastError() != hipSuccess) return SSM_ERR_HIP;
+  }
   hipError_t e = hipErrorInvalidValue;
   switch (dstate) {
     case 32: e = run_chunked<32>(p, stream); break;

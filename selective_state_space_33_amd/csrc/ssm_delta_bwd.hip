@@ -6,6 +6,7 @@
 #include "delta_bwd_kernels.hpp"
 #include "delta_host.hpp"
 #include "host_common.hpp"
+#include "order_kernel.hpp"
 #include "ssm_scan.h"
 
 namespace ssm {
@@ -19,11 +20,11 @@ bool bwd_supported(int64_t batch, int64_t L, int64_t heads, int64_t headdim, int
   return delta_slots(batch, L, nseq) <= 0x7fffffffLL / heads;
 }
 
-// The workspace: [header][amax][images][S0][dS][R][dV][the terms of dla][edges][parts of dA, dbias].
+// The workspace: [header][order of packed sequences][amax][images][S0][dS][R][dV][the terms of dla][edges][parts of dA, dbias].
 struct BwdLayout {
-  size_t amax, img, state, adj, r, dvh, oterm, gterm, lterm, edge, part, total;
+  size_t order, amax, img, state, adj, r, dvh, oterm, gterm, lterm, edge, part, total;
 };
-BwdLayout bwd_layout(int64_t rows, int64_t slots, int64_t heads, int64_t headdim, int64_t dstate) {
+BwdLayout bwd_layout(int64_t rows, int64_t nseq, int64_t slots, int64_t heads, int64_t headdim, int64_t dstate) {
   const size_t cells = static_cast<size_t>(slots) * heads, tiles = headdim / 16;
   BwdLayout l = {};
   size_t at = kDeltaHeader;
@@ -32,6 +33,7 @@ BwdLayout bwd_layout(int64_t rows, int64_t slots, int64_t heads, int64_t headdim
     at += (bytes + 255) & ~static_cast<size_t>(255);
     return here;
   };
+  l.order = take(delta_order_bytes(nseq));
   l.amax = take(static_cast<size_t>(rows) * heads * 4);
   l.img = take(cells * kBwdImgBytes);
   l.state = take(cells * tiles * (dstate / 32) * 2 * kFrag);
@@ -82,7 +84,7 @@ extern "C" size_t ssm_delta_bwd_workspace_size(int64_t batch, int64_t L, int64_t
   if (!delta_shape_supported(rows, L, heads, headdim, dstate) ||
       !bwd_supported(batch, L, heads, headdim, dstate, nseq, dt))
     return 0;
-  return bwd_layout(rows, delta_slots(batch, L, nseq), heads, headdim, dstate).total;
+  return bwd_layout(rows, nseq, delta_slots(batch, L, nseq), heads, headdim, dstate).total;
 }
 
 extern "C" ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
@@ -109,7 +111,7 @@ extern "C" ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* 
     return SSM_ERR_INVALID_ARG;
   if (!bwd_supported(batch, L, heads, headdim, dstate, cu_seqlens ? nseq : 0, dt)) return SSM_ERR_UNSUPPORTED;
   const int64_t rows = cu_seqlens ? nseq : batch, slots = delta_slots(batch, L, cu_seqlens ? nseq : 0);
-  const BwdLayout l = bwd_layout(rows, slots, heads, headdim, dstate);
+  const BwdLayout l = bwd_layout(rows, cu_seqlens ? nseq : 0, slots, heads, headdim, dstate);
   if (!workspace || workspace_bytes < l.total || !delta_aligned(workspace, 256)) return SSM_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
   DeltaBwdParams bp = {};
@@ -123,6 +125,7 @@ extern "C" ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* 
   p.bias = delta_bias;
   p.h0 = initial_state;
   p.cu = cu_seqlens;
+  p.order = reinterpret_cast<int*>(ws + l.order);
   p.img = ws + l.img;
   p.words = reinterpret_cast<unsigned*>(ws);
   p.amax = reinterpret_cast<unsigned*>(ws + l.amax);
@@ -154,6 +157,11 @@ extern "C" ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* 
   bp.edge = reinterpret_cast<float*>(ws + l.edge);
   bp.part = reinterpret_cast<float*>(ws + l.part);
   bp.tiles = headdim / 16;
+  if (cu_seqlens) {
+    hipLaunchKernelGGL(packed_order_kernel, dim3(1), dim3(kOrderBins), 0, stream, p.cu, static_cast<int>(nseq), L,
+                       p.order);
+    if (hipGetLastError() != hipSuccess) return SSM_ERR_HIP;
+  }
   hipError_t e = hipErrorInvalidValue;
   switch (dstate) {
     case 32: e = run_bwd<32>(bp, stream); break;
