@@ -16,6 +16,7 @@ hand-off wait ran out.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -151,6 +152,8 @@ def _check(t: Optional[torch.Tensor], name: str, dtype, shape, device):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return  # (in one step: small calls are bound by the host)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
@@ -164,6 +167,31 @@ def _check(t: Optional[torch.Tensor], name: str, dtype, shape, device):
 def _resolve(device, stream):
     """The torch stream the kernels run on: `stream`, or the device's current stream."""
     return torch.cuda.current_stream(device) if stream is None else stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _place(device, stream):
+    """The torch stream the kernels run on, as _resolve, and a context in which it and its device are current: nothing
+    to enter when they are already."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, expected a GPU")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+        if device.index == torch.cuda.current_device():
+            return stream, _HERE
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return stream, torch.cuda.stream(stream)
+
+
+def _workspace(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace
 
 
 def _ws_bytes(workspace) -> int:
@@ -533,22 +561,21 @@ def ssm_delta_fwd(q, k, v, delta, A, beta, delta_bias=None, softplus: bool = Tru
                                                                         initial_state, cu_seqlens)
     dev, dt = v.device, v.dtype
     code = _dtype_code(dt)
-    s = _resolve(dev, stream)
-    with torch.cuda.stream(s):
+    s, here = _place(dev, stream)
+    with here:
         if y is None:
             y = torch.empty_like(v)
         if final_state is None and return_final_state:
             final_state = torch.empty((rows, heads, headdim, dstate), dtype=torch.float32, device=dev)
         need = ssm_delta_fwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq, dt)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(y, "y", dt, (batch, L, heads, headdim), dev)
-    _check(final_state, "final_state", torch.float32, (rows, heads, headdim, dstate), dev)
-    rc = lib().ssm_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta), _ptr(delta_bias),
-                             1 if softplus else 0, 1 if sigmoid else 0, dstate ** -0.5 if scale is None else scale,
-                             _ptr(initial_state), _ptr(cu_seqlens), nseq, _ptr(y), _ptr(final_state), batch, L,
-                             heads, headdim, ngroups, dstate, code, _ptr(workspace), _ws_bytes(workspace),
-                             s.cuda_stream)
+        workspace = _workspace(workspace, need, dev)
+        _check(y, "y", dt, (batch, L, heads, headdim), dev)
+        _check(final_state, "final_state", torch.float32, (rows, heads, headdim, dstate), dev)
+        rc = lib().ssm_delta_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta), _ptr(delta_bias),
+                                 1 if softplus else 0, 1 if sigmoid else 0, dstate ** -0.5 if scale is None else scale,
+                                 _ptr(initial_state), _ptr(cu_seqlens), nseq, _ptr(y), _ptr(final_state), batch, L,
+                                 heads, headdim, ngroups, dstate, code, _ptr(workspace), _ws_bytes(workspace),
+                                 s.cuda_stream)
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_delta_fwd")
     return y, final_state
@@ -574,8 +601,8 @@ def ssm_delta_bwd(q, k, v, delta, A, beta, dy, delta_bias=None, softplus: bool =
     code = _dtype_code(dt)
     _check(dy, "dy", dt, (batch, L, heads, headdim), dev)
     _check(dfinal_state, "dfinal_state", torch.float32, (rows, heads, headdim, dstate), dev)
-    s = _resolve(dev, stream)
-    with torch.cuda.stream(s):
+    s, here = _place(dev, stream)
+    with here:
         # tokens of no sequence are not written by the call
         new = torch.empty_like if cu_seqlens is None else torch.zeros_like
         g = dict(dq=new(q), dk=new(k), dv=new(v), ddelta=new(delta), dA=torch.empty_like(A), dbeta=new(beta),
@@ -583,14 +610,13 @@ def ssm_delta_bwd(q, k, v, delta, A, beta, dy, delta_bias=None, softplus: bool =
                  dinitial_state=(torch.empty((rows, heads, headdim, dstate), dtype=torch.float32, device=dev)
                                  if (initial_state is not None or want_dinitial_state) else None))
         need = ssm_delta_bwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq, dt)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    rc = lib().ssm_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta), _ptr(delta_bias),
-                             1 if softplus else 0, 1 if sigmoid else 0, dstate ** -0.5 if scale is None else scale,
-                             _ptr(dy), _ptr(dfinal_state), _ptr(initial_state), _ptr(cu_seqlens), nseq, _ptr(g["dq"]),
-                             _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddelta"]), _ptr(g["dA"]), _ptr(g["dbeta"]),
-                             _ptr(g["ddelta_bias"]), _ptr(g["dinitial_state"]), batch, L, heads, headdim, ngroups,
-                             dstate, code, _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
+        workspace = _workspace(workspace, need, dev)
+        rc = lib().ssm_delta_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta), _ptr(delta_bias),
+                                 1 if softplus else 0, 1 if sigmoid else 0, dstate ** -0.5 if scale is None else scale,
+                                 _ptr(dy), _ptr(dfinal_state), _ptr(initial_state), _ptr(cu_seqlens), nseq,
+                                 _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
+                                 _ptr(g["dbeta"]), _ptr(g["ddelta_bias"]), _ptr(g["dinitial_state"]), batch, L, heads,
+                                 headdim, ngroups, dstate, code, _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_delta_bwd")
     return g
@@ -613,15 +639,15 @@ def ssm_delta_update(state, q, k, v, delta, A, beta, delta_bias=None, softplus: 
         _check(t, name, dt, shp, dev)
     _check(A, "A", torch.float32, (heads,), dev)
     _check(delta_bias, "delta_bias", torch.float32, (heads,), dev)
-    s = _resolve(dev, stream)
-    if y is None:
-        with torch.cuda.stream(s):
+    s, here = _place(dev, stream)
+    with here:
+        if y is None:
             y = torch.empty_like(v)
-    _check(y, "y", dt, (batch, heads, headdim), dev)
-    rc = lib().ssm_delta_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta),
-                                _ptr(delta_bias), 1 if softplus else 0, 1 if sigmoid else 0,
-                                dstate ** -0.5 if scale is None else scale, _ptr(y), batch, heads, headdim, ngroups,
-                                dstate, code, s.cuda_stream)
+        _check(y, "y", dt, (batch, heads, headdim), dev)
+        rc = lib().ssm_delta_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(delta), _ptr(A), _ptr(beta),
+                                    _ptr(delta_bias), 1 if softplus else 0, 1 if sigmoid else 0,
+                                    dstate ** -0.5 if scale is None else scale, _ptr(y), batch, heads, headdim, ngroups,
+                                    dstate, code, s.cuda_stream)
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_delta_update")
     return y
@@ -648,13 +674,13 @@ def ssm_gated_norm_fwd(x, z, weight, group: Optional[int] = None, eps: float = 1
     Returns y like x."""
     rows, dim, group, shared = _gated_args(x, z, weight, group)
     code = _dtype_code(x.dtype)
-    s = _resolve(x.device, stream)
-    if y is None:
-        with torch.cuda.stream(s):
+    s, here = _place(x.device, stream)
+    with here:
+        if y is None:
             y = torch.empty_like(x)
-    _check(y, "y", x.dtype, x.shape, x.device)
-    rc = lib().ssm_gated_norm_fwd(_ptr(x), _ptr(z), _ptr(weight), shared, 1 if gate_first else 0, eps, _ptr(y), rows,
-                                  dim, group, code, s.cuda_stream)
+        _check(y, "y", x.dtype, x.shape, x.device)
+        rc = lib().ssm_gated_norm_fwd(_ptr(x), _ptr(z), _ptr(weight), shared, 1 if gate_first else 0, eps, _ptr(y),
+                                      rows, dim, group, code, s.cuda_stream)
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_gated_norm_fwd")
     return y
@@ -670,16 +696,15 @@ def ssm_gated_norm_bwd(x, z, weight, dy, group: Optional[int] = None, eps: float
     rows, dim, group, shared = _gated_args(x, z, weight, group)
     dev, code = x.device, _dtype_code(x.dtype)
     _check(dy, "dy", x.dtype, x.shape, dev)
-    s = _resolve(dev, stream)
-    with torch.cuda.stream(s):
+    s, here = _place(dev, stream)
+    with here:
         g = dict(dx=torch.empty_like(x), dz=None if z is None else torch.empty_like(z),
                  dweight=torch.empty_like(weight))
         need = int(lib().ssm_gated_norm_bwd_workspace_size(rows, dim, group, code))
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    rc = lib().ssm_gated_norm_bwd(_ptr(x), _ptr(z), _ptr(weight), shared, 1 if gate_first else 0, eps, _ptr(dy),
-                                  _ptr(g["dx"]), _ptr(g["dz"]), _ptr(g["dweight"]), rows, dim, group, code,
-                                  _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
+        workspace = _workspace(workspace, need, dev)
+        rc = lib().ssm_gated_norm_bwd(_ptr(x), _ptr(z), _ptr(weight), shared, 1 if gate_first else 0, eps, _ptr(dy),
+                                      _ptr(g["dx"]), _ptr(g["dz"]), _ptr(g["dweight"]), rows, dim, group, code,
+                                      _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_gated_norm_bwd")
     return g
@@ -705,18 +730,18 @@ def ssm_residual_norm_fwd(x, residual, weight, scale=None, post_weight=None, eps
     defaults to float32.  Returns (y like x, residual_out)."""
     rows, dim = _residual_args(x, residual, weight, scale, post_weight)
     dev, code = x.device, _dtype_code(x.dtype)
-    s = _resolve(dev, stream)
-    with torch.cuda.stream(s):
+    s, here = _place(dev, stream)
+    with here:
         if y is None:
             y = torch.empty_like(x)
         if residual_out is None:
             residual_out = torch.empty_like(x if residual is None else residual,
                                             dtype=torch.float32 if residual is None else residual.dtype)
-    _check(y, "y", x.dtype, x.shape, dev)
-    _check(residual_out, "residual_out", residual_out.dtype if residual is None else residual.dtype, x.shape, dev)
-    rc = lib().ssm_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(scale), _ptr(post_weight), _ptr(weight), eps,
-                                     _ptr(y), _ptr(residual_out), rows, dim, code, _dtype_code(residual_out.dtype),
-                                     s.cuda_stream)
+        _check(y, "y", x.dtype, x.shape, dev)
+        _check(residual_out, "residual_out", residual_out.dtype if residual is None else residual.dtype, x.shape, dev)
+        rc = lib().ssm_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(scale), _ptr(post_weight), _ptr(weight), eps,
+                                         _ptr(y), _ptr(residual_out), rows, dim, code, _dtype_code(residual_out.dtype),
+                                         s.cuda_stream)
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_residual_norm_fwd")
     return y, residual_out
@@ -734,18 +759,17 @@ def ssm_residual_norm_bwd(x, residual_out, weight, dy, dresidual_out=None, scale
     dev, code, rcode = x.device, _dtype_code(x.dtype), _dtype_code(residual_out.dtype)
     _check(dy, "dy", x.dtype, x.shape, dev)
     _check(dresidual_out, "dresidual_out", residual_out.dtype, x.shape, dev)
-    s = _resolve(dev, stream)
-    with torch.cuda.stream(s):
+    s, here = _place(dev, stream)
+    with here:
         g = dict(dx=torch.empty_like(x), dresidual=torch.empty_like(residual_out) if want_dresidual else None,
                  dweight=torch.empty_like(weight), dscale=None if scale is None else torch.empty_like(scale),
                  dpost_weight=None if post_weight is None else torch.empty_like(post_weight))
         need = int(lib().ssm_residual_norm_bwd_workspace_size(rows, dim, code, rcode))
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    rc = lib().ssm_residual_norm_bwd(_ptr(x), _ptr(residual_out), _ptr(scale), _ptr(post_weight), _ptr(weight), eps,
-                                     _ptr(dy), _ptr(dresidual_out), _ptr(g["dx"]), _ptr(g["dresidual"]),
-                                     _ptr(g["dscale"]), _ptr(g["dpost_weight"]), _ptr(g["dweight"]), rows, dim, code,
-                                     rcode, _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
+        workspace = _workspace(workspace, need, dev)
+        rc = lib().ssm_residual_norm_bwd(_ptr(x), _ptr(residual_out), _ptr(scale), _ptr(post_weight), _ptr(weight), eps,
+                                         _ptr(dy), _ptr(dresidual_out), _ptr(g["dx"]), _ptr(g["dresidual"]),
+                                         _ptr(g["dscale"]), _ptr(g["dpost_weight"]), _ptr(g["dweight"]), rows, dim,
+                                         code, rcode, _ptr(workspace), _ws_bytes(workspace), s.cuda_stream)
     if rc != SSM_OK:
         raise SSMError(rc, "ssm_residual_norm_bwd")
     return g
