@@ -48,6 +48,27 @@ template <class IO, int VW> __device__ __forceinline__ void vec_load(const void*
     unpack<IO, VW>(raw_load<IO, VW>(base, idx), o);
   }
 }
+// The same kept as it is in memory until get(): half the registers of a bf16 vector.
+template <class IO, int VW> struct Held {
+  Raw<IO, VW> v;
+  __device__ __forceinline__ void clear() { v = Raw<IO, VW>{}; }
+  __device__ __forceinline__ void load(const void* base, int64_t idx) { v = raw_load<IO, VW>(base, idx); }
+  __device__ __forceinline__ void get(float* o) const { unpack<IO, VW>(v, o); }
+  __device__ __forceinline__ void again() {}
+};
+template <> struct Held<BF16, 8> {
+  u32x4_t v;
+  __device__ __forceinline__ void clear() { v = u32x4_t{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const void* base, int64_t idx) {
+    v = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(base) + idx);
+  }
+  __device__ __forceinline__ void get(float* o) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[2 * i] = bf16_lo(v[i]), o[2 * i + 1] = bf16_hi(v[i]);
+  }
+  // before a second get(): keeps the compiler from holding the first one's values instead
+  __device__ __forceinline__ void again() { asm("" : "+v"(v)); }
+};
 template <class IO, int VW> __device__ __forceinline__ void vec_store(void* base, int64_t idx, const float* v) {
   if constexpr (VW == 8 && sizeof(Raw<IO, 1>) == 2) {
     *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(base) + idx) = u32x4_t{
@@ -225,50 +246,56 @@ __global__ void __launch_bounds__(kNormThreads) gated_norm_bwd_kernel(GatedNormP
     const int64_t row = r0 + team;
     const bool live = row < s.rows;
     const int64_t base = row * s.dim + me.col;
-    float x[NV][VW], z[NV][VW], dy[NV][VW], sum[2] = {0.0f, 0.0f};
+    Held<IO, VW> hx[NV], hz[NV], hdy[NV];
+    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int i = 0; i < VW; ++i) x[j][i] = z[j][i] = dy[j][i] = 0.0f;
+      hx[j].clear(), hz[j].clear(), hdy[j].clear();
       if (live && me.on[j]) {
-        vec_load<IO, VW>(p.x, base + me.at[j], x[j]);
-        vec_load<IO, VW>(p.dy, base + me.at[j], dy[j]);
-        if (p.z) vec_load<IO, VW>(p.z, base + me.at[j], z[j]);
+        hx[j].load(p.x, base + me.at[j]);
+        hdy[j].load(p.dy, base + me.at[j]);
+        if (p.z) hz[j].load(p.z, base + me.at[j]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      float x[VW], z[VW], dy[VW];
+      hx[j].get(x), hz[j].get(z), hdy[j].get(dy);
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
         float f = 1.0f, d = 0.0f;
-        if (p.z) silu_parts(z[j][i], f, d);
-        const float t = p.gate_first ? x[j][i] * f : x[j][i];
-        const float m = (p.gate_first ? dy[j][i] : dy[j][i] * f) * w[j][i];
+        if (p.z) silu_parts(z[i], f, d);
+        const float t = p.gate_first ? x[i] * f : x[i];
+        const float m = (p.gate_first ? dy[i] : dy[i] * f) * w[j][i];
         if (me.on[j]) {
           sum[0] = __builtin_fmaf(t, t, sum[0]);
           sum[1] = __builtin_fmaf(m, t, sum[1]);
         }
       }
+    }
     team_sum<2>(sum, s.T, red, par);
     const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum[0], inv, p.eps));
     const float c = sum[1] * inv * rstd;  // mean(m n)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!live || !me.on[j]) continue;
+      float x[VW], z[VW], dy[VW];
+      hx[j].again(), hz[j].again(), hdy[j].again();
+      hx[j].get(x), hz[j].get(z), hdy[j].get(dy);
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
         float f = 1.0f, d = 0.0f;
-        if (p.z) silu_parts(z[j][i], f, d);
-        const float n = (p.gate_first ? x[j][i] * f : x[j][i]) * rstd;
-        const float dn = p.gate_first ? dy[j][i] : dy[j][i] * f;
+        if (p.z) silu_parts(z[i], f, d);
+        const float n = (p.gate_first ? x[i] * f : x[i]) * rstd;
+        const float dn = p.gate_first ? dy[i] : dy[i] * f;
         dw[j][i] = __builtin_fmaf(dn, n, dw[j][i]);
         const float dt = rstd * __builtin_fmaf(-n, c, dn * w[j][i]);
-        const float dzv = p.gate_first ? dt * x[j][i] * d : dy[j][i] * n * w[j][i] * d;
-        x[j][i] = p.gate_first ? dt * f : dt;
-        z[j][i] = dzv;
+        const float dzv = p.gate_first ? dt * x[i] * d : dy[i] * n * w[j][i] * d;
+        x[i] = p.gate_first ? dt * f : dt;
+        z[i] = dzv;
       }
-      vec_store<IO, VW>(p.dx, base + me.at[j], x[j]);
-      if (p.dz) vec_store<IO, VW>(p.dz, base + me.at[j], z[j]);
+      vec_store<IO, VW>(p.dx, base + me.at[j], x);
+      if (p.dz) vec_store<IO, VW>(p.dz, base + me.at[j], z);
     }
   }
   team_partials<NV, VW>(dw, s, me, lds, p.part);
@@ -381,15 +408,17 @@ __global__ void __launch_bounds__(kNormThreads) residual_norm_bwd_kernel(Residua
     const int64_t row = r0 + team;
     const bool live = row < s.rows;
     const int64_t base = row * s.dim;
-    float x[NV][VW], r[NV][VW], g[NV][VW], dr[NV][VW], sum[2] = {0.0f, 0.0f};
+    Held<IO, VW> hx[NV], hg[NV];
+    float r[NV][VW], dr[NV][VW], sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      hx[j].clear(), hg[j].clear();
 #pragma unroll
-      for (int i = 0; i < VW; ++i) x[j][i] = r[j][i] = g[j][i] = dr[j][i] = 0.0f;
+      for (int i = 0; i < VW; ++i) r[j][i] = dr[j][i] = 0.0f;
       if (live && me.on[j]) {
-        vec_load<IO, VW>(p.x, base + me.at[j], x[j]);
+        hx[j].load(p.x, base + me.at[j]);
         vec_load<RIO, VW>(p.residual, base + me.at[j], r[j]);
-        vec_load<IO, VW>(p.dy, base + me.at[j], g[j]);
+        hg[j].load(p.dy, base + me.at[j]);
         if (p.dres_out) vec_load<RIO, VW>(p.dres_out, base + me.at[j], dr[j]);
       }
     }
@@ -397,35 +426,41 @@ __global__ void __launch_bounds__(kNormThreads) residual_norm_bwd_kernel(Residua
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (me.on[j]) {
-        float w[VW];
+        float w[VW], g[VW];
         vec_load<F32, VW>(p.weight, me.at[j], w);
+        hg[j].get(g);
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
           sum[0] = __builtin_fmaf(r[j][i], r[j][i], sum[0]);
-          sum[1] = __builtin_fmaf(g[j][i] * w[i], r[j][i], sum[1]);
+          sum[1] = __builtin_fmaf(g[i] * w[i], r[j][i], sum[1]);
         }
       }
     team_sum<2>(sum, s.T, red, par);
     const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum[0], inv, p.eps));
     const float c = sum[1] * inv * rstd;
     sum[0] = sum[1] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!me.on[j]) continue;
-      float w[VW], sc[VW], pw[VW];
-      vec_load<F32, VW>(p.weight, me.at[j], w);
+    // scale and post_weight of a vector, 1 where there is none
+    auto factors = [&](int j, float (&sc)[VW], float (&pw)[VW]) {
 #pragma unroll
       for (int i = 0; i < VW; ++i) sc[i] = pw[i] = 1.0f;
       if (p.scale) vec_load<F32, VW>(p.scale, me.at[j], sc);
       if (p.post_weight) vec_load<F32, VW>(p.post_weight, me.at[j], pw);
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!me.on[j]) continue;
+      float w[VW], sc[VW], pw[VW], g[VW], x[VW];
+      vec_load<F32, VW>(p.weight, me.at[j], w);
+      factors(j, sc, pw);
+      hg[j].again();
+      hg[j].get(g), hx[j].get(x);
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
         const float n = r[j][i] * rstd;
-        dw[j][i] = __builtin_fmaf(g[j][i], n, dw[j][i]);
-        dr[j][i] += rstd * __builtin_fmaf(-n, c, g[j][i] * w[i]);
-        g[j][i] = dr[j][i] * sc[i] * pw[i];  // into the block's output, past the post weight
-        sum[0] = __builtin_fmaf(x[j][i], x[j][i], sum[0]);
-        sum[1] = __builtin_fmaf(g[j][i], x[j][i], sum[1]);
+        dw[j][i] = __builtin_fmaf(g[i], n, dw[j][i]);
+        dr[j][i] += rstd * __builtin_fmaf(-n, c, g[i] * w[i]);
+        sum[0] = __builtin_fmaf(x[i], x[i], sum[0]);
+        sum[1] = __builtin_fmaf(dr[j][i] * sc[i] * pw[i], x[i], sum[1]);
       }
       if (live && p.dres) vec_store<RIO, VW>(p.dres, base + me.at[j], dr[j]);
     }
@@ -438,19 +473,19 @@ __global__ void __launch_bounds__(kNormThreads) residual_norm_bwd_kernel(Residua
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!live || !me.on[j]) continue;
-      float sc[VW], pw[VW];
-#pragma unroll
-      for (int i = 0; i < VW; ++i) sc[i] = pw[i] = 1.0f;
-      if (p.scale) vec_load<F32, VW>(p.scale, me.at[j], sc);
-      if (p.post_weight) vec_load<F32, VW>(p.post_weight, me.at[j], pw);
+      float sc[VW], pw[VW], x[VW];
+      factors(j, sc, pw);
+      hx[j].again();
+      hx[j].get(x);
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
-        const float n = x[j][i] * xr;  // x itself without a norm behind the block
+        const float n = x[i] * xr;  // x itself without a norm behind the block
         dsc[j][i] = __builtin_fmaf(dr[j][i], n * pw[i], dsc[j][i]);
         dpw[j][i] = __builtin_fmaf(dr[j][i] * sc[i], n, dpw[j][i]);
-        g[j][i] = xr * __builtin_fmaf(-n, xc, g[j][i]);
+        // past the post weight, into the block's output
+        x[i] = xr * __builtin_fmaf(-n, xc, dr[j][i] * sc[i] * pw[i]);
       }
-      vec_store<IO, VW>(p.dx, base + me.at[j], g[j]);
+      vec_store<IO, VW>(p.dx, base + me.at[j], x);
     }
   }
   const int64_t plane = static_cast<int64_t>(s.slots) * s.dim;

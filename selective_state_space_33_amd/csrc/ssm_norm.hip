@@ -25,23 +25,36 @@ struct NormPlan {
   NormSplit s;
 };
 
-// Workgroups per column group of a backward: four workgroups per CU over all
-// groups (each leaves one partial row of weight gradients, so more cost HBM).
-int64_t norm_bwd_slots(int64_t rows, int64_t ngroups) {
-  const int64_t want = nm_ceil(4 * device_cu_count(), ngroups);
+enum NormPass { kNormFwd, kNormGatedBwd, kNormResidualBwd };
+
+// Workgroups per CU over all column groups, each walking its rows: a forward's
+// eight cost nothing but their start.  A backward's each leave a partial row
+// of weight gradients, and a second round of them waits for the first: as many
+// as the kernel's registers let share a CU, by the elements of a thread (8, 16,
+// 24, 32).  16384 x 1536, 24 elements, gated: three 53 us, four 57; 12289 x
+// 2560, 24 elements, residual: two 142 us, four 150.
+constexpr int kNormMaxPerCu = 5;
+int norm_per_cu(NormPass pass, int elems) {
+  if (pass == kNormFwd) return 8;
+  const int n = (pass == kNormGatedBwd ? 6 : 5) - (elems + 7) / 8;
+  return n < 2 ? 2 : n;
+}
+int64_t norm_slots(int64_t rows, int64_t ngroups, int per_cu) {
+  const int64_t want = nm_ceil(per_cu * device_cu_count(), ngroups);
   return want < rows ? want : rows;
 }
 
 // VW elements per vector (1 where a pointer or the row does not allow 16-byte
 // accesses); T the fewest threads that hold a group in at most four vectors
-// each (eight elements with VW = 1), so that a wavefront serves several short
+// each (eight elements with VW = 1; three in the residual backward, where a
+// fourth leaves a CU one workgroup), so that a wavefront serves several short
 // groups without a barrier; wider teams only while rows alone do not give
 // every CU a workgroup.
-NormPlan plan_norm(int64_t rows, int64_t dim, int64_t group, int vw, int64_t slots_cap) {
+NormPlan plan_norm(int64_t rows, int64_t dim, int64_t group, int vw, NormPass pass) {
   NormPlan pl = {};
   pl.VW = vw;
   const int64_t nvec = nm_ceil(group, vw);
-  const int64_t pref = vw == 1 ? 8 : 4, cap = kNormMaxElems / vw;
+  const int64_t pref = vw == 1 ? 8 : (pass == kNormResidualBwd ? 3 : 4), cap = kNormMaxElems / vw;
   int64_t T = 1;
   while (T < 16 && T < nvec) T *= 2;
   while (T < kNormThreads && nm_ceil(nvec, T) > pref) T *= 2;
@@ -60,9 +73,8 @@ NormPlan plan_norm(int64_t rows, int64_t dim, int64_t group, int vw, int64_t slo
   pl.s.ngroups = static_cast<int>(ngroups);
   pl.s.T = static_cast<int>(T);
   pl.s.teams = static_cast<int>(kNormThreads / T);
-  int64_t slots = nm_ceil(rows, pl.s.teams);
-  if (slots > slots_cap) slots = slots_cap;
-  pl.s.slots = static_cast<int>(slots);
+  const int64_t most = norm_slots(rows, ngroups, norm_per_cu(pass, pl.NV * vw)), slots = nm_ceil(rows, pl.s.teams);
+  pl.s.slots = static_cast<int>(slots < most ? slots : most);
   return pl;
 }
 
@@ -139,8 +151,6 @@ bool nm_unsupported(int64_t rows, int64_t dim, int64_t group) {
   return group > kNormMaxGroup || rows > 0x7fffffffLL || dim > 0x7fffffffLL;
 }
 
-int64_t fwd_slots_cap(int64_t ngroups) { return nm_ceil(8 * device_cu_count(), ngroups); }
-
 }  // namespace
 }  // namespace ssm
 
@@ -156,8 +166,7 @@ extern "C" ssm_status_t ssm_gated_norm_fwd(const void* x, const void* z, const f
   if (nm_unsupported(rows, dim, group)) return SSM_ERR_UNSUPPORTED;
   const int vw = static_cast<int>(16 / es);
   const void* const ptrs[] = {x, z, weight, y};
-  const NormPlan pl =
-      plan_norm(rows, dim, group, nm_vec_ok(group, vw, ptrs) ? vw : 1, fwd_slots_cap(dim / group));
+  const NormPlan pl = plan_norm(rows, dim, group, nm_vec_ok(group, vw, ptrs) ? vw : 1, kNormFwd);
   GatedNormParams p = {};
   p.x = x;
   p.z = z;
@@ -173,7 +182,7 @@ extern "C" ssm_status_t ssm_gated_norm_fwd(const void* x, const void* z, const f
 
 extern "C" size_t ssm_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, ssm_dtype_t dt) {
   if (nm_shape_bad(rows, dim, group, 0.0f) || !nm_dtype_ok(dt) || nm_unsupported(rows, dim, group)) return 0;
-  return kNormHeader + nm_al256(static_cast<size_t>(norm_bwd_slots(rows, dim / group)) * dim * sizeof(float));
+  return kNormHeader + nm_al256(static_cast<size_t>(norm_slots(rows, dim / group, kNormMaxPerCu)) * dim * sizeof(float));
 }
 
 extern "C" ssm_status_t ssm_gated_norm_bwd(const void* x, const void* z, const float* weight, int shared_flag,
@@ -192,8 +201,7 @@ extern "C" ssm_status_t ssm_gated_norm_bwd(const void* x, const void* z, const f
     return SSM_ERR_INVALID_ARG;
   const int vw = static_cast<int>(16 / es);
   const void* const ptrs[] = {x, z, weight, dy, dx, dz};
-  const NormPlan pl =
-      plan_norm(rows, dim, group, nm_vec_ok(group, vw, ptrs) ? vw : 1, norm_bwd_slots(rows, dim / group));
+  const NormPlan pl = plan_norm(rows, dim, group, nm_vec_ok(group, vw, ptrs) ? vw : 1, kNormGatedBwd);
   GatedNormParams p = {};
   p.x = x;
   p.z = z;
@@ -235,7 +243,7 @@ extern "C" ssm_status_t ssm_residual_norm_fwd(const void* x, const void* residua
   if (nm_unsupported(rows, dim, dim) || (dt == SSM_DTYPE_F32 && res_dt != SSM_DTYPE_F32)) return SSM_ERR_UNSUPPORTED;
   const int vw = static_cast<int>(16 / es);
   const void* const ptrs[] = {x, residual, scale, post_weight, weight, y, residual_out};
-  const NormPlan pl = plan_norm(rows, dim, dim, nm_vec_ok(dim, vw, ptrs) ? vw : 1, fwd_slots_cap(1));
+  const NormPlan pl = plan_norm(rows, dim, dim, nm_vec_ok(dim, vw, ptrs) ? vw : 1, kNormFwd);
   ResidualNormParams p = {};
   p.x = x;
   p.residual = residual;
@@ -256,7 +264,7 @@ extern "C" size_t ssm_residual_norm_bwd_workspace_size(int64_t rows, int64_t dim
   if (nm_shape_bad(rows, dim, dim, 0.0f) || !nm_dtype_ok(dt) || !nm_dtype_ok(res_dt) ||
       nm_unsupported(rows, dim, dim) || (dt == SSM_DTYPE_F32 && res_dt != SSM_DTYPE_F32))
     return 0;
-  return kNormHeader + nm_al256(3 * static_cast<size_t>(norm_bwd_slots(rows, 1)) * dim * sizeof(float));
+  return kNormHeader + nm_al256(3 * static_cast<size_t>(norm_slots(rows, 1, kNormMaxPerCu)) * dim * sizeof(float));
 }
 
 extern "C" ssm_status_t ssm_residual_norm_bwd(const void* x, const void* residual_out, const float* scale,
@@ -281,7 +289,7 @@ extern "C" ssm_status_t ssm_residual_norm_bwd(const void* x, const void* residua
     return SSM_ERR_INVALID_ARG;
   const int vw = static_cast<int>(16 / es);
   const void* const ptrs[] = {x, residual_out, scale, post_weight, weight, dy, dresidual_out, dx, dresidual};
-  const NormPlan pl = plan_norm(rows, dim, dim, nm_vec_ok(dim, vw, ptrs) ? vw : 1, norm_bwd_slots(rows, 1));
+  const NormPlan pl = plan_norm(rows, dim, dim, nm_vec_ok(dim, vw, ptrs) ? vw : 1, kNormResidualBwd);
   ResidualNormParams p = {};
   p.x = x;
   p.residual = residual_out;
