@@ -38,16 +38,6 @@
 
 namespace ssm {
 
-// The scale of a unit's gradients: it brings their largest magnitude to [16, 32), within what fp32 holds on both
-// sides; 1 where there is none, or none that is finite.  (What is summed from them stays thousands of times below the
-// largest fp16, and the lo part of a pair, whose last place is 2^-24, keeps its bits down to 2^-3.)
-__device__ __forceinline__ float grad_scale(unsigned amax_bits) {
-  const int e = static_cast<int>(amax_bits >> 23) - 127;
-  if (amax_bits == 0u || e > 127) return 1.0f;
-  const int s = e < -96 ? 100 : (e > 104 ? -100 : 4 - e);
-  return __uint_as_float(static_cast<unsigned>(s + 127) << 23);
-}
-
 // bf16 values as floats, times a scale.
 __device__ __forceinline__ f32x4_t bf16x4_f32(u32x2_t v, float s) {
   return f32x4_t{bf16_lo(v[0]) * s, bf16_hi(v[0]) * s, bf16_lo(v[1]) * s, bf16_hi(v[1]) * s};
@@ -126,7 +116,7 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t blocks = (p.P + 16 * W - 1) / (16 * W);
   const DeltaUnit un = delta_unit(p, blocks);
-  const int64_t seq = un.seq, h = un.h, unit = seq * p.H + h, g = h / (p.H / p.G);
+  const int64_t seq = un.seq, h = un.h, unit = seq * p.H + h, g = key_head(h, p.H, p.G);
   const int col = static_cast<int>(un.block * W + w) * 16;
   const DeltaSeq sq = delta_seq(p.cu, seq, p.L, p.chunks);
   const int nchunks = static_cast<int>((sq.len + kDeltaC - 1) / kDeltaC);
@@ -134,6 +124,7 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
   const int rowe32 = static_cast<int>(rowe), krow32 = static_cast<int>(krow);
   const int yrow = (lr * rowe32 + 4 * lq) * 2;
   const float sc = nchunks > 0 ? grad_scale(p.amax[unit]) : 1.0f, inv = 1.0f / sc;
+  const float both = nchunks > 0 ? inv / p.vscale[unit] : 1.0f;  // of what S0 or R enters too
 
   // ---- dS (scaled): channel col + lr, states 16 d + 4 lq .. + 3
   f32x4_t S[DT];
@@ -426,13 +417,13 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     });
     // ---- the terms of dla, and dV's rows
     rsrc_t rt = ls.take(true);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(lt, lr) * inv), rt, term_at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(lt, lr) * both), rt, term_at, 0, 0);
     rt = gs.take(true);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(gt, lr) * -inv), rt, term_at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(gt, lr) * -both), rt, term_at, 0, 0);
     e0 += e1;  // its diagonal: each channel's <dS, S0>
     const float diag = (lr & 2) ? ((lr & 1) ? e0[3] : e0[2]) : ((lr & 1) ? e0[1] : e0[0]);
     rt = es.take(true);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lq == (lr >> 2) ? diag * fade * inv : 0.0f), rt, mine4, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lq == (lr >> 2) ? diag * fade * both : 0.0f), rt, mine4, 0, 0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       vt[t] *= inv;
@@ -494,13 +485,13 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
   uint16_t *const sK = lds.k, *const sQ = lds.q;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t id = xcd_order(blockIdx.x, p.slots * p.G);
-  const int64_t slot = id / p.G, g = id % p.G, rep = p.H / p.G;
+  const unsigned groups = static_cast<unsigned>(p.G), id = xcd_order(blockIdx.x, static_cast<unsigned>(p.slots) * groups);
+  const int64_t slot = id / groups, g = id % groups, rep = static_cast<unsigned>(p.H) / groups;
   int64_t s = 0;
   if (p.cu) {
     s = delta_slot_seq(p.cu, p.rows, p.L, slot);
   } else {
-    s = slot / p.chunks;
+    s = static_cast<unsigned>(slot) / static_cast<unsigned>(p.chunks);
   }
   const DeltaSeq sq = delta_seq(p.cu, s, p.L, p.chunks);
   const int64_t c0 = (slot - sq.slot) * kDeltaC;
@@ -538,7 +529,7 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
     const int lane = tid & 63, lr = lane & 15, lq = lane >> 4;
-    const float sc = grad_scale(p.amax[s * p.H + h]), inv = 1.0f / sc;
+    const float scy = grad_scale(p.amax[s * p.H + h]), sc = scy * p.vscale[s * p.H + h], inv = 1.0f / sc;
     const int tbytes = static_cast<int>(bp.tiles * kFrag);
     const rsrc_t rr = make_rsrc(bp.r + cell * bp.tiles * (4 * kFrag), 4 * tbytes);
     const rsrc_t rv = make_rsrc(bp.dvh + cell * bp.tiles * (4 * kFrag), 4 * tbytes);
@@ -606,7 +597,7 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
         u32x4_t y8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f16x2_t hv = __builtin_convertvector((f32x2_t){bf16_lo(g_y[i]) * sc, bf16_hi(g_y[i]) * sc}, f16x2_t);
+          const f16x2_t hv = __builtin_convertvector((f32x2_t){bf16_lo(g_y[i]) * scy, bf16_hi(g_y[i]) * scy}, f16x2_t);
           y8[i] = __builtin_bit_cast(uint32_t, hv);
         }
         lds_store_paired(&lds.y[row * kGradLd], cc, y8);

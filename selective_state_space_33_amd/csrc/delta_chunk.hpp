@@ -46,9 +46,8 @@ constexpr int kImgThi = 0;                   // T, fp16 hi
 constexpr int kImgTlo = 6 * kFrag;           // T, fp16 lo
 constexpr int kImgP = 12 * kFrag;            // P, fp16
 constexpr int kImgGrow = 18 * kFrag;         // e^{cs_t}
-constexpr int kImgOut = kImgGrow + 256;      // scale e^{cs_t}
-constexpr int kImgLeft = kImgGrow + 512;     // e^{cs_C - cs_t} b_t (0 behind the sequence's end)
-constexpr int kImgBytes = kImgGrow + 768;
+constexpr int kImgLeft = kImgGrow + 256;     // e^{cs_C - cs_t} b_t (0 behind the sequence's end)
+constexpr int kImgBytes = kImgGrow + 512;
 // The backward's image: the same fragments of T (for its walk forward), then T's and P's transposes (for its walk back;
 // P without b), each a pair, and the gates.
 constexpr float kBwdPScale = 16.0f;          // P is kept 16 times as large, away from the last places of fp16
@@ -189,6 +188,24 @@ __device__ __forceinline__ int64_t delta_slot_seq(const int64_t* cu, int64_t n, 
   return lo;
 }
 
+// What is linear in the values (or in the gradients) may have any magnitude, but passes through fp16 pairs.  So values
+// and initial states are scaled by the power of two that brings their largest magnitude to [2, 4), dY and dfinal to
+// [16, 32), and results scaled back, all exactly.  (States and sums stay thousands of times below the largest fp16; the
+// lo part of a pair, whose last place is 2^-24, keeps its bits down to 2^-3.)  The scale is 1 where nothing, or something
+// not finite, is the largest; it stays between 2^-60 and 2^60, so that products of two stay in fp32.
+__device__ __forceinline__ float unit_scale(unsigned amax_bits, int target) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127;
+  if (amax_bits == 0u || e > 127) return 1.0f;
+  const int s = target - e < -60 ? -60 : (target - e > 60 ? 60 : target - e);
+  return __uint_as_float(static_cast<unsigned>(s + 127) << 23);
+}
+__device__ __forceinline__ float grad_scale(unsigned amax_bits) { return unit_scale(amax_bits, 4); }
+// (lower for heads wider than 256: the gradients take dy . u over all channels as an fp16)
+__device__ __forceinline__ float value_scale(unsigned amax_bits, int64_t P) {
+  const int wide = 56 - __builtin_clzll(static_cast<unsigned long long>(P - 1));  // log2(P / 256), rounded up
+  return unit_scale(amax_bits, 1 - (wide > 0 ? wide : 0));
+}
+
 // A channel tile that the head does not have is addressed here: behind every
 // resource (they are cut to this length, and a chunk's offsets, 64 rows of at
 // most 2^23 bytes, stay below half of it), so loads return zero and stores are
@@ -197,8 +214,8 @@ constexpr int kPastEnd = 0x40000000;
 
 // Workgroups are dealt round-robin to the eight XCDs; giving each XCD a run of
 // consecutive units lets neighbours that read the same rows share its L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
-  const int64_t q = n / 8, r = n % 8, x = i % 8;
+__device__ __forceinline__ unsigned xcd_order(unsigned i, unsigned n) {
+  const unsigned q = n / 8, r = n % 8, x = i % 8;
   return x * q + (x < r ? x : r) + i / 8;
 }
 
@@ -208,10 +225,16 @@ __device__ __forceinline__ int64_t xcd_order(int64_t i, int64_t n) {
 struct DeltaUnit {
   int64_t seq, h, block;
 };
+__device__ __forceinline__ int64_t key_head(int64_t h, int64_t H, int64_t G) {
+  return static_cast<unsigned>(h) / (static_cast<unsigned>(H) / static_cast<unsigned>(G));
+}
+// (Workgroups are counted in 32 bits, which the host sees to, and divided so: a division of 64 bits is a hundred
+// instructions.)
 template <class P> __device__ __forceinline__ DeltaUnit delta_unit(const P& p, int64_t blocks) {
-  const int64_t id = p.cu ? static_cast<int64_t>(blockIdx.x) : xcd_order(blockIdx.x, p.rows * p.H * blocks);
-  const int64_t unit = id / blocks, s = unit / p.H;
-  return {p.cu ? static_cast<int64_t>(p.order[s]) : s, unit % p.H, id % blocks};
+  const unsigned nb = static_cast<unsigned>(blocks), H = static_cast<unsigned>(p.H);
+  const unsigned id = p.cu ? blockIdx.x : xcd_order(blockIdx.x, static_cast<unsigned>(p.rows) * H * nb);
+  const unsigned unit = id / nb, s = unit / H;
+  return {p.cu ? p.order[s] : s, unit - s * H, id - unit * nb};
 }
 
 struct DeltaChunkParams {
@@ -229,7 +252,11 @@ struct DeltaChunkParams {
   void* y;
   char* img;           // [slots][H][kImgBytes]
   unsigned* words;     // workspace header
-  unsigned* amax;      // [rows][H]: bits of max |dy|, |dfinal| of a unit (backward)
+  // backward: bits of the largest |v| of a chunk (of the first one |initial state| too) [slots][H], of the largest |dy|
+  // and |dfinal| of a unit [rows][H]; the scale of a unit's values
+  unsigned* vmax;
+  unsigned* amax;
+  float* vscale;
   int64_t rows;        // sequences
   int64_t L, H, G, P;
   int64_t chunks;      // chunks per batch row (no cu)

@@ -53,23 +53,24 @@ template <int J> __device__ __forceinline__ void prep_column(float* sM, int lr, 
 template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkParams p) {
   constexpr int IMG = BWD ? kBwdImgBytes : kImgBytes, GATES = BWD ? kBwdGates : kImgGrow;
   constexpr int SB = DK + 8;  // bf16 row stride
-  constexpr int ROWS = 2 * kDeltaC * SB * 2, MAT = kDeltaC * kPrepLd * 4;  // bytes
+  constexpr int ROWS = kDeltaC * SB * 2, MAT = kDeltaC * kPrepLd * 4;  // bytes
   __shared__ __attribute__((aligned(16))) char sMem[ROWS > MAT ? ROWS : MAT];
   uint16_t* const sK = reinterpret_cast<uint16_t*>(sMem);
-  uint16_t* const sQ = sK + kDeltaC * SB;
   float* const sM = reinterpret_cast<float*>(sMem);
   __shared__ __attribute__((aligned(16))) float sChi[kDeltaC], sClo[kDeltaC], sBeta[kDeltaC];
+  __shared__ unsigned sTop;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
   if (p.words && blockIdx.x == 0 && tid < 4) p.words[tid] = 0u;
-  const int64_t id = xcd_order(blockIdx.x, static_cast<int64_t>(p.slots) * p.H);
-  const int64_t slot = id / p.H, h = id % p.H, g = h / (p.H / p.G);
+  if (tid == 0) sTop = 0u;
+  const unsigned heads = static_cast<unsigned>(p.H), id32 = xcd_order(blockIdx.x, static_cast<unsigned>(p.slots) * heads);
+  const int64_t id = id32, slot = id32 / heads, h = id32 % heads, g = key_head(h, p.H, p.G);
   // the sequence of this slot: the last one that starts at or before it
   int64_t s = 0;
   if (p.cu) {
     s = delta_slot_seq(p.cu, p.rows, p.L, slot);
   } else {
-    s = slot / p.chunks;
+    s = static_cast<unsigned>(slot) / static_cast<unsigned>(p.chunks);
   }
   const DeltaSeq sq = delta_seq(p.cu, s, p.L, p.chunks);
   const int64_t c0 = (slot - sq.slot) * kDeltaC;
@@ -77,20 +78,41 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
   const int nt = static_cast<int>(sq.len - c0 < kDeltaC ? sq.len - c0 : kDeltaC);
   const int64_t tok = sq.tok + c0;
 
-  // ---- K, Q (rows behind the end are zero) and the gates
+  // BWD: the first of this thread's pieces of the values (three wavefronts take them): on their way until they are needed
+  const int64_t vrow = p.H * p.P;
+  const rsrc_t rv = make_rsrc(static_cast<const uint16_t*>(p.v) + tok * vrow + h * p.P, ((nt - 1) * vrow + p.P) * 2);
+  const int pieces = static_cast<int>(p.P / 8);
+  auto value_piece = [&](int e) {  // (past the 64th row: past the resource)
+    const int row = e / pieces;
+    const int at = row < kDeltaC ? static_cast<int>((row * vrow + (e - row * pieces) * 8) * 2) : kPastEnd;
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rv, at, 0, 0));
+  };
+  constexpr int EARLY = 6;
+  u32x4_t vv[EARLY];
+  // ---- K and Q (rows behind the end are zero) and the gates.  Of Q a wavefront takes one row tile alone.
+  const int tt = 3 - w;
+  bf16x8_t qf[DK / 32];
   {
     const int64_t rowe = p.G * DK;
     const int64_t base = tok * rowe + g * DK, bytes = ((nt - 1) * rowe + DK) * 2;
     const rsrc_t rk = make_rsrc(static_cast<const uint16_t*>(p.k) + base, bytes);
     const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(p.q) + base, bytes);
     constexpr int PER = kDeltaC * DK / 8 / 256;
-    u32x4_t kv[PER], qv[PER];
+    u32x4_t kv[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = tid + 256 * i, row = e / (DK / 8), col = (e % (DK / 8)) * 8;
-      const int off = static_cast<int>((row * rowe + col) * 2);
-      kv[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0));
-      qv[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
+      kv[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, static_cast<int>((row * rowe + col) * 2), 0, 0));
+    }
+#pragma unroll
+    for (int kk = 0; kk < DK / 32; ++kk)
+      qf[kk] = __builtin_bit_cast(
+          bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(
+                        rq, static_cast<int>(((16 * tt + lr) * rowe + 32 * kk + 8 * lq) * 2), 0, 0));
+    if constexpr (BWD) {
+#pragma unroll
+      for (int i = 0; i < EARLY; ++i) vv[i] = value_piece(w > 0 ? tid - 64 + 192 * i : kDeltaC * pieces);
     }
     if (w == 0) {
       const bool live = lane < nt;
@@ -116,23 +138,22 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
       float* img = reinterpret_cast<float*>(p.img + id * IMG + GATES);
       const float grow = __builtin_amdgcn_exp2f(chi * kLog2e);
       img[lane] = grow;
-      img[64 + lane] = p.scale * grow;
       const float left = __builtin_amdgcn_exp2f(static_cast<float>(end - cs) * kLog2e);
       if constexpr (BWD) {
+        img[64 + lane] = p.scale * grow;
         img[128 + lane] = left;
         img[192 + lane] = b;
         img[256 + lane] = chi;
         img[320 + lane] = static_cast<float>(cs - static_cast<double>(chi));
         if (c0 == 0 && lane == 0) p.amax[s * p.H + h] = 0u;  // before the walk that takes the maximum
       } else {
-        img[128 + lane] = left * b;
+        img[64 + lane] = left * b;
       }
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = tid + 256 * i, row = e / (DK / 8), col = (e % (DK / 8)) * 8;
       *reinterpret_cast<u32x4_t*>(&sK[row * SB + col]) = kv[i];
-      *reinterpret_cast<u32x4_t*>(&sQ[row * SB + col]) = qv[i];
     }
   }
   __syncthreads();
@@ -160,36 +181,33 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
       m[jt][r] = j < t ? sBeta[j] * fade(t, j) * m[jt][r] : 0.0f;
     }
   }
-  // ---- P^T: the tiles of Q K^T leave four consecutive t of token j = lr in a lane, half a fragment
+  // ---- P of token tile tt.  Backward: P^T, from tiles of Q K^T, which leave four consecutive t of token j = lr in a lane,
+  // half a fragment; the half above the diagonal's tile is zero
   if constexpr (BWD) {
-    const int j = 16 * w + lr;
-    for (int m2 = w / 2; m2 < 2; ++m2) {
-      f32x4_t half[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int tt = 2 * m2 + u;
-        f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (tt >= w) {
-#pragma unroll
-          for (int kk = 0; kk < DK / 32; ++kk)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sQ, tt, kk), frag(sK, w, kk), acc, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int t = 16 * tt + 4 * lq + r;
-            acc[r] = j <= t ? p.scale * kBwdPScale * fade(t, j) * acc[r] : 0.0f;
-          }
-        }
-        half[u] = acc;
-      }
+    auto put = [&](int jt, f32x4_t v) {
       f16x8_t hi, lo;
-      split_f16(half[0], half[1], hi, lo);
-      char* out = p.img + id * IMG + kBwdBack + (12 + back_frag(w, m2)) * kFrag + lane * 16;
-      *reinterpret_cast<f16x8_t*>(out) = hi;
-      *reinterpret_cast<f16x8_t*>(out + 6 * kFrag) = lo;
+      split_f16(v, v, hi, lo);
+      char* out = p.img + id * IMG + kBwdBack + (12 + back_frag(jt, tt / 2)) * kFrag + lane * 16 + (tt & 1) * 8;
+      *reinterpret_cast<f16x4_t*>(out) = __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
+      *reinterpret_cast<f16x4_t*>(out + 6 * kFrag) = __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
+    };
+    for (int jt = 0; jt <= tt; ++jt) {
+      f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kk = 0; kk < DK / 32; ++kk)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[kk], frag(sK, jt, kk), acc, 0, 0, 0);
+      const int j = 16 * jt + lr;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * tt + 4 * lq + r;
+        acc[r] = j <= t ? p.scale * kBwdPScale * fade(t, j) * acc[r] : 0.0f;
+      }
+      put(jt, acc);
     }
+    if (!(tt & 1)) put(tt + 1, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
   } else {
-    // ---- P: the tiles of K Q^T leave four consecutive j of token t = lr in a lane, half a fragment
-    const int tt = 3 - w, t = 16 * tt + lr;
+    // the tiles of K Q^T leave four consecutive j of token t = lr in a lane, half a fragment
+    const int t = 16 * tt + lr;
     for (int m2 = 0; m2 <= tt / 2; ++m2) {
       f32x4_t half[2];
 #pragma unroll
@@ -199,11 +217,11 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
         if (jt <= tt) {
 #pragma unroll
           for (int kk = 0; kk < DK / 32; ++kk)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, jt, kk), frag(sQ, tt, kk), acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(sK, jt, kk), qf[kk], acc, 0, 0, 0);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * jt + 4 * lq + r;
-            acc[r] = j <= t ? p.scale * sBeta[j] * fade(t, j) * acc[r] : 0.0f;
+            acc[r] = j <= t ? sBeta[j] * fade(t, j) * acc[r] : 0.0f;
           }
         }
         half[u] = acc;
@@ -213,7 +231,7 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
           pair_f16(half[0], half[1]);
     }
   }
-  __syncthreads();  // K and Q are read
+  __syncthreads();  // K is read
 #pragma unroll
   for (int jt = 0; jt < 4; ++jt)
     if (jt <= w) {
@@ -240,6 +258,30 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) sM[(b0 + i) * kPrepLd + b0 + c] = x[i];
+  } else if constexpr (BWD) {
+    // ---- meanwhile the largest value (magnitudes order as their bits do)
+    unsigned top = 0u;
+    auto take = [&](u32x4_t x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        top = max(top, (x[i] << 16) & 0x7fff0000u);
+        top = max(top, x[i] & 0x7fff0000u);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) take(vv[i]);
+    for (int e = tid - 64 + 192 * EARLY; e < kDeltaC * pieces; e += 192) take(value_piece(e));
+    if (p.h0 && c0 == 0) {
+      const u32x4_t* s0 = reinterpret_cast<const u32x4_t*>(p.h0 + (s * p.H + h) * p.P * DK);
+      for (int64_t e = tid - 64; e < p.P * DK / 4; e += 192) {
+        const u32x4_t x = s0[e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, x[i] & 0x7fffffffu);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = max(top, static_cast<unsigned>(__shfl_xor(static_cast<int>(top), o, 64)));
+    if (lane == 0) atomicMax(&sTop, top);
   }
   __syncthreads();
   if (w == 0)
@@ -249,6 +291,7 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
   else if (w == 2)
     prep_column<2>(sM, lr, lq);
   __syncthreads();
+  if (BWD && tid == 0) p.vmax[id] = sTop;
   // ---- T as fragments, hi + lo
   for (int e = tid; e < 6 * 64; e += 256) {
     const int f = e >> 6, ln = e & 63, row = ln & 15, q4 = 4 * (ln >> 4);

@@ -63,10 +63,12 @@ template <class IO, int DK, int RPT>
 __global__ void __launch_bounds__(64 * kDeltaStepWaves) delta_step_kernel(DeltaStepParams p) {
   constexpr int NC = DK / 32;  // 4-state pieces of a lane: states 32 c + 4 l .. + 3
   const int tid = threadIdx.x, l8 = tid & 7;
-  const int64_t unit = blockIdx.x / p.row_blocks;
-  const int64_t seq = unit / p.H, h = unit % p.H;
-  const int64_t g = h / (p.H / p.G);
-  const int64_t row0 = (blockIdx.x % p.row_blocks) * (kDeltaStepWaves * 8 * RPT) + (tid >> 6) * (8 * RPT) +
+  // (the host keeps the counts in 32 bits)
+  const unsigned nb = static_cast<unsigned>(p.row_blocks), heads = static_cast<unsigned>(p.H);
+  const unsigned unit = blockIdx.x / nb;
+  const int64_t seq = unit / heads, h = unit % heads;
+  const int64_t g = static_cast<unsigned>(h) / (heads / static_cast<unsigned>(p.G));
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x % nb) * (kDeltaStepWaves * 8 * RPT) + (tid >> 6) * (8 * RPT) +
                        ((tid & 63) >> 3);
   int64_t t0 = seq * p.L, t1 = t0 + p.L;
   if (p.cu) {

@@ -39,6 +39,18 @@ struct DeltaStream {
   }
 };
 
+// The larger magnitudes of two pairs of bf16, and the largest of a wavefront's (as integers, which order as they do).
+__device__ __forceinline__ unsigned max_bf16x2(unsigned a, unsigned b) {
+  typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a & 0x7fff7fffu),
+                                                                __builtin_bit_cast(u16x2_t, b & 0x7fff7fffu)));
+}
+__device__ __forceinline__ unsigned wave_max(unsigned v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v = max(v, static_cast<unsigned>(__shfl_xor(static_cast<int>(v), o, 64)));
+  return static_cast<unsigned>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
+}
+
 template <int DK, bool KEEP> struct DeltaWalkLds {
   __attribute__((aligned(16))) uint16_t k[kDeltaC * kRowLd<DK>];
   __attribute__((aligned(16))) uint16_t kt[kDeltaC * kColLd<DK>];
@@ -83,7 +95,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t blocks = (p.P + 16 * W - 1) / (16 * W);  // workgroups per unit
   const DeltaUnit un = delta_unit(p, blocks);
-  const int64_t seq = un.seq, h = un.h, unit = seq * p.H + h, g = h / (p.H / p.G);
+  const int64_t seq = un.seq, h = un.h, unit = seq * p.H + h, g = key_head(h, p.H, p.G);
   const int col = static_cast<int>(un.block * W + w) * 16;  // first channel of this wavefront
   const DeltaSeq sq = delta_seq(p.cu, seq, p.L, p.chunks);
   const int nchunks = static_cast<int>((sq.len + kDeltaC - 1) / kDeltaC);
@@ -91,13 +103,32 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
   const int rowe32 = static_cast<int>(rowe), krow32 = static_cast<int>(krow);  // the host keeps them below 2^22
   const int yrow = (lr * rowe32 + 4 * lq) * 2;
 
+  // ---- the scale of the values and the state.  KEEP: one of the whole unit, from the largest value of each chunk.  The
+  // forward: this tile's own, from the first chunk and the initial state; a chunk with values 512 times larger than the
+  // scale was made for gets a new one (`limit`), to which the state goes over.  (Looking for the largest value before the
+  // walk, as the backward does, read all of v once more: 50 us of 380 at 16384 tokens of 40 heads.)
+  float sc = 1.0f, inv = 1.0f, yscale = p.scale;
+  unsigned vtop = 0u, limit = 0u;  // the largest |v| of the next chunk (a pair of bf16), and what they may be (fp32 bits)
+  auto set_scale = [&](float to) {
+    sc = to;
+    inv = 1.0f / sc;
+    yscale = p.scale * inv;
+    limit = __float_as_uint(512.0f * inv);
+  };
+  if constexpr (KEEP) {
+    unsigned top = 0u;
+    for (int c = lane; c < nchunks; c += 64) top = max(top, p.vmax[(sq.slot + c) * p.H + h]);
+    set_scale(value_scale(wave_max(top), p.P));
+    if (tid == 0 && un.block == 0) p.vscale[unit] = sc;
+  }
+
   // ---- the state: channel col + lr, states 16 d + 4 lq .. + 3
   f32x4_t S[DT];
   const int64_t sbase = (unit * p.P + col + lr) * DK + 4 * lq;
 #pragma unroll
   for (int d = 0; d < DT; ++d) {
     S[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.h0 && col < p.P) S[d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * d);
+    if (p.h0 && col < p.P) S[d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * d) * sc;
   }
 
   // ---- chunk loads, one chunk ahead in registers
@@ -181,6 +212,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       constexpr int t = 2 * ((i - PER - IPER) % 2);
       *reinterpret_cast<u32x2_t*>(&lds_v[w][(16 * t + lr) * 16 + 4 * lq]) = gv[t];
       *reinterpret_cast<u32x2_t*>(&lds_v[w][(16 * t + 16 + lr) * 16 + 4 * lq]) = gv[t + 1];
+      if constexpr (!KEEP)
+        vtop = max_bf16x2(vtop, max_bf16x2(max_bf16x2(gv[t][0], gv[t][1]), max_bf16x2(gv[t + 1][0], gv[t + 1][1])));
     } else {
       constexpr int e = i - PER - IPER - 2, t = 2 * (e % 2);
       __builtin_amdgcn_raw_buffer_store_b64(yo[t], ry, yrow + ctile, 32 * t * rowe32, 0);
@@ -202,6 +235,20 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     load_dy();
   }
   __syncthreads();
+  if constexpr (!KEEP) {
+    if (nchunks > 0) {
+      unsigned top = max(vtop & 0x7fff0000u, vtop << 16);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(S[d][r]) & 0x7fffffffu);
+      top = wave_max(top);
+      set_scale(top == 0u ? 0x1p60f : unit_scale(top, 1));  // nothing yet: the first value sets it
+      vtop = 0u;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) S[d] *= sc;
+    }
+  }
   f16x8_t Sh[KT], Sl[KT];
 #pragma unroll
     for (int kk = 0; kk < KT; ++kk) split_f16(S[2 * kk], S[2 * kk + 1], Sh[kk], Sl[kk]);
@@ -255,7 +302,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     auto finish_x = [&](int t) {
       const float v[4] = {bf16_lo(vq[t][0]), bf16_hi(vq[t][0]), bf16_lo(vq[t][1]), bf16_hi(vq[t][1])};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(-grow[t & 1][r], x[t][r], v[r]);
+      for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(-grow[t & 1][r], x[t][r], v[r] * sc);
       if (t & 1) split_f16(x[t - 1], x[t], Xh[t >> 1], Xl[t >> 1]);
     };
     static_for<STEPS>([&](auto step) {
@@ -290,7 +337,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     f32x4_t left[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      left[t] = img_vec(GATES + 512, t);
+      left[t] = img_vec(KEEP ? GATES + 512 : kImgLeft, t);
       if constexpr (KEEP) left[t] *= img_vec(GATES + 768, t);
     }
     f16x8_t kc[DT];  // K^T, a half of the tokens at a time
@@ -348,7 +395,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     } else {
       Rf[0] = pair_f16(u[0], u[1]), Rf[1] = pair_f16(u[2], u[3]);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) og[t] = *reinterpret_cast<const float*>(&b.img[kImgOut + (16 * t + lr) * 4]);
+      for (int t = 0; t < 4; ++t) og[t] = *reinterpret_cast<const float*>(&b.img[GATES + (16 * t + lr) * 4]);
 #pragma unroll
       for (int f = 0; f < 6; ++f) pf[f] = img_frag(kImgP, f);
     }
@@ -381,10 +428,10 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       const float a1 = (odd ? dots[3] : dots[2]) + __shfl_xor(odd ? dots[2] : dots[3], 16, 64);
       const float dot = (high ? a1 : a0) + __shfl_xor(high ? a0 : a1, 32, 64);
       rkeep = os.take(1);
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot * og[0]), rkeep, lane * 4 + (col < p.P ? 0 : kPastEnd),
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot * og[0] * inv), rkeep, lane * 4 + (col < p.P ? 0 : kPastEnd),
                                             0, 0);
     } else {
-      // ---- Y^T = (Q S0)^T diag(scale e^cs) + R^T P^T
+      // ---- Y^T = ((Q S0)^T diag(e^cs) + R^T P^T) scale
 #pragma unroll
       for (int t = 0; t < 4; ++t) o[t] *= og[t];
 #pragma unroll
@@ -393,8 +440,23 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       for (int t = 2; t < 4; ++t) o[t] = mfma_f16(Rf[1], pf[frag_of(t, 1)], o[t]);
       split_f16(S[DT - 2], S[DT - 1], Sh[KT - 1], Sl[KT - 1]);
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t) {
+        o[t] *= yscale;
         yo[t] = u32x2_t{pack_bf16x2(o[t][0], o[t][1]), pack_bf16x2(o[t][2], o[t][3])};
+      }
+      const unsigned top = max(vtop & 0x7fff0000u, vtop << 16);
+      vtop = 0u;
+      if (__any(top > limit)) {
+        const unsigned all = wave_max(top);
+        if (all < 0x7f800000u) {
+          const float was = inv;
+          set_scale(unit_scale(all, 1));
+#pragma unroll
+          for (int d = 0; d < DT; ++d) S[d] *= sc * was;
+#pragma unroll
+          for (int kk = 0; kk < KT; ++kk) split_f16(S[2 * kk], S[2 * kk + 1], Sh[kk], Sl[kk]);
+        }
+      }
     }
     __syncthreads();
   }
@@ -421,7 +483,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     if (p.hT) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        if (col < p.P) *reinterpret_cast<f32x4_t*>(p.hT + sbase + 16 * d) = S[d];
+        if (col < p.P) *reinterpret_cast<f32x4_t*>(p.hT + sbase + 16 * d) = S[d] * inv;
     }
   }
 }

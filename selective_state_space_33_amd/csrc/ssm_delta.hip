@@ -165,8 +165,9 @@ extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* 
   p.cu = cu_seqlens;
   p.y = y;
   p.words = static_cast<unsigned*>(workspace);
+  // the workspace: header, order of packed sequences, images
   p.order = reinterpret_cast<int*>(static_cast<char*>(workspace) + kDeltaHeader);
-  p.img = static_cast<char*>(workspace) + kDeltaHeader + delta_order_bytes(cu_seqlens ? nseq : 0);
+  p.img = static_cast<char*>(workspace) + kDeltaHeader + delta_order_bytes(nseq);
   p.rows = cu_seqlens ? nseq : batch;
   p.L = L;
   p.H = heads;

@@ -20,9 +20,9 @@ bool bwd_supported(int64_t batch, int64_t L, int64_t heads, int64_t headdim, int
   return delta_slots(batch, L, nseq) <= 0x7fffffffLL / heads;
 }
 
-// The workspace: [header][order of packed sequences][amax][images][S0][dS][R][dV][the terms of dla][edges][parts of dA, dbias].
+// The workspace: [header][order of packed sequences][largest gradients, values' scales, largest values][images][S0][dS][R][dV][the terms of dla][edges][parts of dA, dbias].
 struct BwdLayout {
-  size_t order, amax, img, state, adj, r, dvh, oterm, gterm, lterm, edge, part, total;
+  size_t order, amax, vscale, vmax, img, state, adj, r, dvh, oterm, gterm, lterm, edge, part, total;
 };
 BwdLayout bwd_layout(int64_t rows, int64_t nseq, int64_t slots, int64_t heads, int64_t headdim, int64_t dstate) {
   const size_t cells = static_cast<size_t>(slots) * heads, tiles = headdim / 16;
@@ -35,6 +35,8 @@ BwdLayout bwd_layout(int64_t rows, int64_t nseq, int64_t slots, int64_t heads, i
   };
   l.order = take(delta_order_bytes(nseq));
   l.amax = take(static_cast<size_t>(rows) * heads * 4);
+  l.vscale = take(static_cast<size_t>(rows) * heads * 4);
+  l.vmax = take(cells * 4);
   l.img = take(cells * kBwdImgBytes);
   l.state = take(cells * tiles * (dstate / 32) * 2 * kFrag);
   l.adj = take(cells * tiles * (dstate / 32) * kFrag);
@@ -129,6 +131,8 @@ extern "C" ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* 
   p.img = ws + l.img;
   p.words = reinterpret_cast<unsigned*>(ws);
   p.amax = reinterpret_cast<unsigned*>(ws + l.amax);
+  p.vscale = reinterpret_cast<float*>(ws + l.vscale);
+  p.vmax = reinterpret_cast<unsigned*>(ws + l.vmax);
   p.rows = rows;
   p.L = L;
   p.H = heads;

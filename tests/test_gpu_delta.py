@@ -290,3 +290,30 @@ def test_long_sequence_against_oracle():
     x = I.random_delta_inputs(rng, 1, 2048, 1, 2, 64, 32)
     x["A"] = np.float32([-0.01, -0.5])
     check(x, "bf16", "long, slow fade")
+
+
+@pytest.mark.parametrize("size", [1e-12, 1e-5, 3e4, 1e9])
+def test_values_of_any_magnitude(size):
+    """Values, states and y scale together (by a power of two per row and head): as exact at 1e-12 as at 1, beside a row
+    of zeros and one of ordinary size."""
+    rng = np.random.default_rng(1600)
+    x = I.random_delta_inputs(rng, 3, 200, 2, 4, 64, 48)
+    size = np.array([size, 0.0, 1.0]).reshape(3, 1, 1, 1)
+    x["v"] = I.round_to_bf16((x["v"] * size).astype(np.float32))
+    h0 = (size * rng.standard_normal((3, 4, 48, 64))).astype(np.float32)
+    say(f"delta values of size {size[0, 0, 0, 0]}")
+    y, s = run(x, "bf16", h0)
+    yo, so = D.delta_fwd(**x, initial_state=h0)
+    M, Ms = D.delta_magnitudes(**x, initial_state=h0)
+    for b in (0, 2):
+        (ey, en), es = y_off(host(y)[b], yo[b], M[b], "bf16"), s_off(host(s)[b], so[b], Ms[b])
+        print(f"[parity] row {b}: y {ey:.2f} of its bound, norm {en:.2e}, state {es:.2e}", flush=True)
+        assert ey <= 1 and en <= TOL_NORM["bf16"] and es <= TOL_STATE, (b, ey, en, es)
+    assert not host(y)[1].any() and not host(s)[1].any()
+
+
+@pytest.mark.parametrize("scale", [1e-9, 1e6])
+def test_scale_of_any_magnitude(scale):
+    rng = np.random.default_rng(1610)
+    x = I.random_delta_inputs(rng, 1, 150, 1, 2, 32, 32)
+    check(x, "bf16", f"scale {scale}", scale=scale)

@@ -175,3 +175,20 @@ def test_gradients_against_differences_of_the_forward():
     d = (loss(A, b, h + dirn) - loss(A, b, h - dirn)) / 2     # linear in the state
     got = float((g["dinitial_state"].double() * dirn.double()).sum())
     assert abs(d - got) <= 1e-3 * max(1.0, abs(d)), (d, got)
+
+
+@pytest.mark.parametrize("size", [1e-12, 1e-4, 1e9])
+def test_backward_of_values_of_any_magnitude(size):
+    rng = np.random.default_rng(3700)
+    x = I.random_delta_inputs(rng, 2, 150, 2, 4, 64, 48)
+    x["v"] = I.round_to_bf16((x["v"] * size).astype(np.float32))
+    h0 = (size * rng.standard_normal((2, 4, 48, 64))).astype(np.float32)
+    check(x, f"v ~ {size}", rng=rng, h0=h0)
+
+
+def test_backward_of_wide_heads_pulling_one_way():
+    """All of 1040 channels add up in dy . u: nothing on the way leaves fp16's range."""
+    rng = np.random.default_rng(3710)
+    x = I.random_delta_inputs(rng, 1, 70, 1, 1, 32, 1040)
+    x["v"] = np.full(x["v"].shape, 1.9375, np.float32)
+    check(x, "wide", dy=np.full(x["v"].shape, 0.96875, np.float32))
