@@ -178,7 +178,10 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * w + 4 * lq + r;
-      m[jt][r] = j < t ? sBeta[j] * fade(t, j) * m[jt][r] : 0.0f;
+      // An entry that is not finite stays out of the inverse, where it would reach the rows before its own: the state
+      // and y of its token and all behind it take it from K, P or the fades.
+      const float v = sBeta[j] * fade(t, j) * m[jt][r];
+      m[jt][r] = j < t && __builtin_fabsf(v) <= 3.4e38f ? v : 0.0f;
     }
   }
   // ---- P of token tile tt.  Backward: P^T, from tiles of Q K^T, which leave four consecutive t of token j = lr in a lane,

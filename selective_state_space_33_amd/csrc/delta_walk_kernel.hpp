@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
   // each wavefront's own values, [token][channel], as they are in memory (bf16): written with the next chunk's
   // operands, read transposed at its start
   __shared__ __attribute__((aligned(16))) uint16_t lds_v[W][kDeltaC * 16];
+  __shared__ int lds_first[W][16];  // of each channel, where a chunk's values stop being finite
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t blocks = (p.P + 16 * W - 1) / (16 * W);  // workgroups per unit
@@ -108,7 +109,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
   // scale was made for gets a new one (`limit`), to which the state goes over.  (Looking for the largest value before the
   // walk, as the backward does, read all of v once more: 50 us of 380 at 16384 tokens of 40 heads.)
   float sc = 1.0f, inv = 1.0f, yscale = p.scale;
-  unsigned vtop = 0u, limit = 0u;  // the largest |v| of the next chunk (a pair of bf16), and what they may be (fp32 bits)
+  unsigned limit = 0u;  // what |v| may be (fp32 bits)
+  bool over = false;    // the next chunk has larger ones
   auto set_scale = [&](float to) {
     sc = to;
     inv = 1.0f / sc;
@@ -212,13 +214,29 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       constexpr int t = 2 * ((i - PER - IPER) % 2);
       *reinterpret_cast<u32x2_t*>(&lds_v[w][(16 * t + lr) * 16 + 4 * lq]) = gv[t];
       *reinterpret_cast<u32x2_t*>(&lds_v[w][(16 * t + 16 + lr) * 16 + 4 * lq]) = gv[t + 1];
-      if constexpr (!KEEP)
-        vtop = max_bf16x2(vtop, max_bf16x2(max_bf16x2(gv[t][0], gv[t][1]), max_bf16x2(gv[t + 1][0], gv[t + 1][1])));
+      if constexpr (!KEEP) {
+        const unsigned m = max_bf16x2(max_bf16x2(gv[t][0], gv[t][1]), max_bf16x2(gv[t + 1][0], gv[t + 1][1]));
+        over = over || __any(max(m & 0x7fff0000u, m << 16) > limit);
+      }
     } else {
       constexpr int e = i - PER - IPER - 2, t = 2 * (e % 2);
       __builtin_amdgcn_raw_buffer_store_b64(yo[t], ry, yrow + ctile, 32 * t * rowe32, 0);
       __builtin_amdgcn_raw_buffer_store_b64(yo[t + 1], ry, yrow + ctile, 32 * (t + 1) * rowe32, 0);
     }
+  };
+
+  // the largest |v| of the chunk that this wavefront has staged last
+  auto staged_top = [&] {
+    int own = threadIdx.x;  // (opaque: what only this needs is not carried through the loop)
+    asm volatile("" : "+v"(own));
+    const uint16_t* a = &lds_v[w][(own & 15) * 16 + 4 * ((own & 63) >> 4)];
+    unsigned m = 0u;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const u32x2_t v = *reinterpret_cast<const u32x2_t*>(a + 256 * t);
+      m = max_bf16x2(m, max_bf16x2(v[0], v[1]));
+    }
+    return max(m & 0x7fff0000u, m << 16);
   };
 
   if (nchunks > 0) {
@@ -237,14 +255,14 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
   __syncthreads();
   if constexpr (!KEEP) {
     if (nchunks > 0) {
-      unsigned top = max(vtop & 0x7fff0000u, vtop << 16);
+      unsigned top = staged_top();
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(S[d][r]) & 0x7fffffffu);
       top = wave_max(top);
       set_scale(top == 0u ? 0x1p60f : unit_scale(top, 1));  // nothing yet: the first value sets it
-      vtop = 0u;
+      over = false;
 #pragma unroll
       for (int d = 0; d < DT; ++d) S[d] *= sc;
     }
@@ -329,6 +347,40 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       slot(IC<j>{});
     });
     finish_x(3);
+    // An X that is not finite (a NaN in padding behind the tokens that count, say) would meet T's zeros in the next
+    // products, and R's in those of P.  So X from a channel's first such token on is taken out here, and y from there on
+    // and the state are set to NaN at the end.
+    bool broken = false;
+    if constexpr (!KEEP) {
+      f16x2_t sum = {static_cast<_Float16>(0.0f), static_cast<_Float16>(0.0f)};  // of zeros times X
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f16x2_t v = {Xh[m][2 * e], Xh[m][2 * e + 1]};
+          sum = __builtin_elementwise_fma(v, f16x2_t{static_cast<_Float16>(0.0f), static_cast<_Float16>(0.0f)}, sum);
+        }
+      broken = __any(sum[0] != sum[0] || sum[1] != sum[1]);
+      if (broken) {
+        int own = threadIdx.x & 63;  // (opaque, as above)
+        asm volatile("" : "+v"(own));
+        auto token = [&](int m, int e) { return 32 * m + (e < 4 ? 0 : 16) + 4 * (own >> 4) + (e & 3); };
+        int first = kDeltaC;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            first = !(__builtin_fabsf(static_cast<float>(Xh[m][e])) <= 65504.0f) ? min(first, token(m, e)) : first;
+        first = min(first, __shfl_xor(first, 16, 64));
+        first = min(first, __shfl_xor(first, 32, 64));
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (token(m, e) >= first) Xh[m][e] = Xl[m][e] = static_cast<_Float16>(0.0f);
+        lds_first[w][own & 15] = first;
+      }
+    }
     // ---- R = T X
     __builtin_amdgcn_sched_barrier(0);
     read_t(3);
@@ -440,22 +492,36 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       for (int t = 2; t < 4; ++t) o[t] = mfma_f16(Rf[1], pf[frag_of(t, 1)], o[t]);
       split_f16(S[DT - 2], S[DT - 1], Sh[KT - 1], Sl[KT - 1]);
 #pragma unroll
+      for (int t = 0; t < 4; ++t) o[t] *= yscale;
+      if (broken) {
+        int own = threadIdx.x & 63;
+        asm volatile("" : "+v"(own));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int from = lds_first[w][4 * (own >> 4) + r];  // of this lane's channels of y
+#pragma unroll
+          for (int t = 0; t < 4; ++t) o[t][r] = 16 * t + (own & 15) >= from ? __builtin_nanf("") : o[t][r];
+        }
+      }
+#pragma unroll
       for (int t = 0; t < 4; ++t) {
-        o[t] *= yscale;
         yo[t] = u32x2_t{pack_bf16x2(o[t][0], o[t][1]), pack_bf16x2(o[t][2], o[t][3])};
       }
-      const unsigned top = max(vtop & 0x7fff0000u, vtop << 16);
-      vtop = 0u;
-      if (__any(top > limit)) {
-        const unsigned all = wave_max(top);
-        if (all < 0x7f800000u) {
+      if (broken || over) {
+        int own = threadIdx.x & 15;
+        asm volatile("" : "+v"(own));
+        float by = broken && lds_first[w][own] < kDeltaC ? __builtin_nanf("") : 1.0f;
+        const unsigned top = wave_max(staged_top());
+        if (over && top < 0x7f800000u) {
           const float was = inv;
-          set_scale(unit_scale(all, 1));
-#pragma unroll
-          for (int d = 0; d < DT; ++d) S[d] *= sc * was;
-#pragma unroll
-          for (int kk = 0; kk < KT; ++kk) split_f16(S[2 * kk], S[2 * kk + 1], Sh[kk], Sl[kk]);
+          set_scale(unit_scale(top, 1));
+          by *= sc * was;
         }
+        over = false;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) S[d] *= by;
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) split_f16(S[2 * kk], S[2 * kk + 1], Sh[kk], Sl[kk]);
       }
     }
     __syncthreads();

@@ -317,3 +317,32 @@ def test_scale_of_any_magnitude(scale):
     rng = np.random.default_rng(1610)
     x = I.random_delta_inputs(rng, 1, 150, 1, 2, 32, 32)
     check(x, "bf16", f"scale {scale}", scale=scale)
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("where", ["q", "k", "v", "delta", "beta"])
+@pytest.mark.parametrize("token", [0, 69, 111, 128])
+def test_garbage_in_padding_leaves_what_is_before_it(where, token, value):
+    """A NaN or an infinity in a token (of padding, say) reaches it and what follows it, and no token before it, other
+    row, head or (from v) channel: there the results are those of the clean call, bit for bit."""
+    rng = np.random.default_rng(1620)
+    x = I.random_delta_inputs(rng, 2, 140, 2, 4, 64, 48)
+    say(f"delta {value} in {where} at {token}")
+    y0, s0 = run(x, "bf16")
+    head = 1 if where in "qk" else 2
+    x[where] = x[where].copy()
+    x[where][(1, token, head) + ((5,) if where in "qkv" else ())] = -value if where == "delta" else value
+    y, s = run(x, "bf16")
+    same = y == y0
+    heads = [2, 3] if where in "qk" else [2]
+    if where == "v":
+        assert not torch.isfinite(y[1, token:, 2, 5]).any() and not torch.isfinite(s[1, 2, 5]).any()
+        same[1, token:, 2, 5] = True
+    elif where in "qk" or np.isnan(value):
+        assert not torch.isfinite(y[1, token, heads]).any()
+        same[1, token:, heads] = True
+    else:       # an infinite step or beta is a fade or a gate of its limit: nothing, 0 or 1
+        same[1, token:, heads] = True
+    assert bool(same.all())
+    if where == "k" or (where in ("delta", "beta") and np.isnan(value)):
+        assert not torch.isfinite(s[1, heads]).any()
