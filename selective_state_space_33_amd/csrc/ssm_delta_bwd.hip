@@ -59,12 +59,9 @@ template <int DK> hipError_t run_bwd(const DeltaBwdParams& bp, hipStream_t s) {
   hipLaunchKernelGGL((delta_prep_kernel<DK, true>), dim3(cells), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // (eight or four wavefronts a workgroup as in the forward)
-  if (bp.tiles > 4 && walks > static_cast<unsigned>(device_cu_count()))
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 8, true>), dim3(static_cast<unsigned>(p.rows * p.H * ((bp.tiles + 7) / 8))),
-                       dim3(512), 0, s, bp);
-  else
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 4, true>), dim3(walks), dim3(256), 0, s, bp);
+  // Four wavefronts a workgroup always: eight would have 256 registers each, and spill (160 heads of 128 channels, dstate
+  // 128, 64 chunks in two rounds of workgroups: 528 us; with eight, in one, 718 us).
+  hipLaunchKernelGGL((delta_walk_kernel<DK, W, true>), dim3(walks), dim3(64 * W), 0, s, bp);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((delta_bwd_walk_kernel<DK, W>), dim3(walks), dim3(64 * W), 0, s, bp);
