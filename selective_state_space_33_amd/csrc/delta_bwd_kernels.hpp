@@ -504,8 +504,8 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
   const int64_t krow = p.G * DK, rowe = p.H * p.P;
   const int64_t kb = tok * krow + g * DK, kbytes = ((nt - 1) * krow + DK) * 2;
   constexpr int KPER = kDeltaC * DK / 8 / 256;
-  u32x4_t g_k[KPER], g_q[KPER];
   {
+    u32x4_t g_k[KPER], g_q[KPER];
     const rsrc_t rk = make_rsrc(static_cast<const uint16_t*>(p.k) + kb, kbytes);
     const rsrc_t rq = make_rsrc(static_cast<const uint16_t*>(p.q) + kb, kbytes);
 #pragma unroll
@@ -514,6 +514,12 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
       const int off = static_cast<int>((row * krow + cc) * 2);
       g_k[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0));
       g_q[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
+    }
+#pragma unroll
+    for (int i = 0; i < KPER; ++i) {
+      const int e = tid + 256 * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
+      *reinterpret_cast<u32x4_t*>(&sK[row * CL + cc]) = bf16x8_as_f16(g_k[i]);
+      *reinterpret_cast<u32x4_t*>(&sQ[row * CL + cc]) = bf16x8_as_f16(g_q[i]);
     }
   }
   const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -573,14 +579,6 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
     load(0);
     f32x4_t g_g = zero;  // the gates, a lane four
     if (tid < 6 * 16) g_g = *reinterpret_cast<const f32x4_t*>(p.img + cell * kBwdImgBytes + kBwdGates + tid * 16);
-    if (hh == 0) {  // K and Q, loaded ahead of all of this
-#pragma unroll
-      for (int i = 0; i < KPER; ++i) {
-        const int e = tid + 256 * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
-        *reinterpret_cast<u32x4_t*>(&sK[row * CL + cc]) = bf16x8_as_f16(g_k[i]);
-        *reinterpret_cast<u32x4_t*>(&sQ[row * CL + cc]) = bf16x8_as_f16(g_q[i]);
-      }
-    }
     // dla's terms of each token (a lane) over every fourth tile
     double og = 0.0, lt = 0.0, edge = 0.0;
     for (int64_t t = w; t < bp.tiles; t += 4) {
