@@ -20,11 +20,14 @@
 // b or by a fade.
 //
 // Four kernels: delta_prep_kernel<., true> (T, P0, gates of all chunks);
-// delta_bwd_walk_kernel<., ., false> walks forward and keeps each chunk's S0 and
-// R; <., ., true> walks back, a wavefront holding 16 channels of dS as the
+// delta_walk_kernel<., ., true> walks forward and keeps each chunk's S0 and R;
+// delta_bwd_walk_kernel walks back, a wavefront holding 16 channels of dS as the
 // forward's holds S, writes dV and keeps it and dS; delta_grad_kernel forms dq,
 // dk, db and dla of all chunks at once, a workgroup per chunk and key head,
-// which sums its heads in order.
+// which sums its heads in order.  2 x 4096 tokens of 40 heads of 128 channels,
+// dstate 128: 80, 270, 352 and 300 us.  The walks are bound by their chunks'
+// chain (64 chunks, 4.2 and 5.5 us each, 160 of the 256 CUs), the last by
+// latency at two workgroups a CU (740 MB, 2.5 TB/s).
 //
 // Precision.  What goes from chunk to chunk, dV and every term of dla is a pair
 // of fp16 (22 bits) in fp32 accumulators.  dY and what is linear in it may have

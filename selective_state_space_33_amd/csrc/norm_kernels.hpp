@@ -23,7 +23,12 @@
 // sums and products are fp32; outputs are rounded once, to nearest even.
 //
 // What bounds them: HBM.  A row costs its loads and stores plus ~10 VALU
-// instructions an element (the sigmoid's exp and rcp among them).
+// instructions an element (the sigmoid's exp and rcp among them).  A large
+// copy moves 4.9 TB/s here; the gated norm over 16384 x 5120 in heads of 128
+// 4.5 (111 us), its backward over 16384 x 1536 4.7 and 5 us for the weight's
+// sums (53), the residual norm's backward over 12289 x 2560 with a norm behind
+// the block 3.9 and 5 (145: 24 elements of four tensors and three sums a
+// thread leave a CU two workgroups).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -49,7 +49,8 @@ int64_t norm_slots(int64_t rows, int64_t ngroups, int per_cu) {
 // each (eight elements with VW = 1; three in the residual backward, where a
 // fourth leaves a CU one workgroup), so that a wavefront serves several short
 // groups without a barrier; wider teams only while rows alone do not give
-// every CU a workgroup.
+// every CU a workgroup (256 rows, residual forward, wider / not: of 2560 4.5 /
+// 5.0 us, of 1536 3.7 / 4.8).
 NormPlan plan_norm(int64_t rows, int64_t dim, int64_t group, int vw, NormPass pass) {
   NormPlan pl = {};
   pl.VW = vw;
