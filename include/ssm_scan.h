@@ -413,12 +413,19 @@ ssm_status_t ssm_scan_trap_bwd(const void* u, const void* delta, const float* A,
  *   q, k and the states 16-byte aligned, everything else to its element.
  *   dstate 32, 64, 96, 128, 192 or 256, any headdim; else UNSUPPORTED.
  *   y must not alias an input.
- * Plans: long bf16 sequences with dstate <= 128 and headdim a multiple of 16
- * run in chunks of 64 tokens on the matrix cores; everything else runs token
- * by token in fp32.  In the chunked plan q, k, v and the state pass through
- * fp16 pairs hi + lo (22 significant bits; q and k convert exactly), so they
- * must stay below 65504 in magnitude, and what is smaller than 2^-24 counts
- * as zero; beyond, the outputs become inf or NaN.  Errors as ssm_ssd_fwd. */
+ * Plans: bf16 sequences of more than 16 tokens (on average) with dstate <=
+ * 128, headdim a multiple of 16, heads * headdim and heads * dstate up to
+ * 2^22 and v and y 8-byte aligned run in chunks of 64 tokens on the matrix
+ * cores; everything else runs token by token in fp32.  In the chunked plan q
+ * and k pass through fp16 (exactly from 2^-14 to 65504 in magnitude; smaller
+ * elements to a multiple of 2^-24, larger ones make what they reach inf or
+ * NaN); v, the states and y may have any magnitude (they are scaled by powers
+ * of two), with 22 significant bits on the states' way, relative to the
+ * largest value and state of 16 channels.  A token that is not finite (in
+ * padding, say) reaches itself and the tokens and states behind it, never a
+ * token before it; from v only its own channel.
+ * workspace: ssm_delta_fwd_workspace_size() bytes, 256-byte aligned; calls
+ * that may overlap need one each.  Errors as ssm_ssd_fwd. */
 ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
                            const void* beta, const float* delta_bias, int softplus_flag, int sigmoid_flag,
                            float scale, const float* initial_state, const int64_t* cu_seqlens, int64_t nseq,
@@ -449,11 +456,13 @@ size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int
  *   headdim and heads * dstate up to 2^22; else UNSUPPORTED.  q, k, v, dy, dq,
  *   dk, dv and the states 16-byte aligned, everything else to its element.  Only
  *   dfinal_state and dinitial_state may be the same buffer; no other output
- *   may alias anything.  q, k, v and the states must stay below 65504 in
- *   magnitude (ssm_delta_fwd); dy and dfinal_state may have any magnitude:
- *   each (row, head) is scaled by a power of two of its own.  workspace:
- *   ssm_delta_bwd_workspace_size() bytes, 256-byte aligned (at dstate =
- *   headdim = 128 about 162 KB per chunk of 64 tokens and head). */
+ *   may alias anything.  q and k pass through fp16 as in ssm_delta_fwd; v and
+ *   the initial state, and dy and dfinal_state, may have any magnitude: each
+ *   (row, head) is scaled by powers of two of its own.  An input that is not
+ *   finite makes every gradient of its row (or sequence) and head unusable.
+ *   workspace: ssm_delta_bwd_workspace_size() bytes, 256-byte aligned (at
+ *   dstate = headdim = 128 about 206 KB per chunk of 64 tokens and head);
+ *   calls that may overlap need one each. */
 ssm_status_t ssm_delta_bwd(const void* q, const void* k, const void* v, const void* delta, const float* A,
                            const void* beta, const float* delta_bias, int softplus_flag, int sigmoid_flag,
                            float scale, const void* dy, const float* dfinal_state, const float* initial_state,

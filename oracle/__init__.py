@@ -18,6 +18,10 @@ the automatic-differentiation backward, with planted mistakes in
 ``tests/test_oracle_mutants.py``.
 ``ssd.py`` is the Mamba-2 SSD layer in its quadratic masked-matrix form (numpy),
 pinned in ``tests/test_oracle_ssd.py`` against the C oracle's recurrence.
+``delta.py`` is the gated delta rule and its adjoint, token by token (numpy, fp64),
+and ``norms.py`` the RMS norms around a layer; they are pinned in
+``tests/test_oracle_delta.py`` and ``tests/test_oracle_norms.py`` against hand
+examples, closed forms, the C oracle and central finite differences.
 
 Pin status.  The trapezoidal (Mamba-3) scan is partly pinned: its tests fix the
 step as read (impulse response, constant-input closed form, second-order

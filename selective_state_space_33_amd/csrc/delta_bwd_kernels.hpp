@@ -127,7 +127,8 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
   const int rowe32 = static_cast<int>(rowe), krow32 = static_cast<int>(krow);
   const int yrow = (lr * rowe32 + 4 * lq) * 2;
   const float sc = nchunks > 0 ? grad_scale(p.amax[unit]) : 1.0f, inv = 1.0f / sc;
-  const float both = nchunks > 0 ? inv / p.vscale[unit] : 1.0f;  // of what S0 or R enters too
+  // of what R enters too, and of what S0 does
+  const float both = nchunks > 0 ? inv / p.vscale[unit] : 1.0f, state = both / kBwdStateUp;
 
   // ---- dS (scaled): channel col + lr, states 16 d + 4 lq .. + 3
   f32x4_t S[DT];
@@ -422,11 +423,11 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     rsrc_t rt = ls.take(true);
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(lt, lr) * both), rt, term_at, 0, 0);
     rt = gs.take(true);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(gt, lr) * -both), rt, term_at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum_rows16(gt, lr) * -state), rt, term_at, 0, 0);
     e0 += e1;  // its diagonal: each channel's <dS, S0>
     const float diag = (lr & 2) ? ((lr & 1) ? e0[3] : e0[2]) : ((lr & 1) ? e0[1] : e0[0]);
     rt = es.take(true);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lq == (lr >> 2) ? diag * fade * both : 0.0f), rt, mine4, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lq == (lr >> 2) ? diag * fade * state : 0.0f), rt, mine4, 0, 0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       vt[t] *= inv;
@@ -619,8 +620,10 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
           if (e >= SP) continue;
           // fragment kk, lane (v, quad): states 32 kk + 4 quad .. + 3 and + 16
           const int at = (16 * u + (f & 15)) * CL + 32 * (f >> 6) + 4 * ((f >> 4) & 3);
-          *reinterpret_cast<u32x2_t*>(&lds.s[at]) = u32x2_t{g_s[i][0], g_s[i][1]};
-          *reinterpret_cast<u32x2_t*>(&lds.s[at + 16]) = u32x2_t{g_s[i][2], g_s[i][3]};
+          const u32x4_t s0 = __builtin_bit_cast(
+              u32x4_t, __builtin_bit_cast(f16x8_t, g_s[i]) * static_cast<_Float16>(1.0f / kBwdStateUp));
+          *reinterpret_cast<u32x2_t*>(&lds.s[at]) = u32x2_t{s0[0], s0[1]};
+          *reinterpret_cast<u32x2_t*>(&lds.s[at + 16]) = u32x2_t{s0[2], s0[3]};
           *reinterpret_cast<u32x2_t*>(&lds.a[at]) = u32x2_t{g_a[i][0], g_a[i][1]};
           *reinterpret_cast<u32x2_t*>(&lds.a[at + 16]) = u32x2_t{g_a[i][2], g_a[i][3]};
         }

@@ -51,6 +51,10 @@ constexpr int kImgBytes = kImgGrow + 512;
 // The backward's image: the same fragments of T (for its walk forward), then T's and P's transposes (for its walk back;
 // P without b), each a pair, and the gates.
 constexpr float kBwdPScale = 16.0f;          // P is kept 16 times as large, away from the last places of fp16
+// Beside its values' scale the backward's forward walk holds the state 32 times as large: its elements are smaller than
+// the values that make them, and the last place of a pair's lo part is 2^-24 (states of 128 x 128 were off by 3.5e-7
+// without it, by 2.2e-7 with it).
+constexpr float kBwdStateUp = 32.0f;
 constexpr int kBwdBack = 12 * kFrag;         // T^T hi, T^T lo, P^T hi, P^T lo: six fragments each
 constexpr int kBwdGates = kBwdBack + 24 * kFrag;
 // (64 floats each: e^{cs_t}, scale e^{cs_t}, e^{cs_C - cs_t}, b_t, and cs_t as a pair hi, lo)
@@ -185,9 +189,9 @@ __device__ __forceinline__ int64_t delta_slot_seq(const int64_t* cu, int64_t n, 
 }
 
 // What is linear in the values (or in the gradients) may have any magnitude, but passes through fp16 pairs.  So values
-// and initial states are scaled by the power of two that brings their largest magnitude to [2, 4), dY and dfinal to
-// [16, 32), and results scaled back, all exactly.  (States and sums stay thousands of times below the largest fp16; the
-// lo part of a pair, whose last place is 2^-24, keeps its bits down to 2^-3.)  The scale is 1 where nothing, or something
+// and initial states are scaled by the power of two that brings their largest magnitude to [32, 64) (the backward's to
+// [2, 4)), dY and dfinal to [16, 32), and results scaled back, all exactly.  (Above, states and sums have room up to the
+// largest fp16, 65504; the lo part of a pair, whose last place is 2^-24, keeps its bits down to 2^-3.)  The scale is 1 where nothing, or something
 // not finite, is the largest; it stays between 2^-60 and 2^60, so that products of two stay in fp32.
 __device__ __forceinline__ float unit_scale(unsigned amax_bits, int target) {
   const int e = static_cast<int>(amax_bits >> 23) - 127;

@@ -32,6 +32,12 @@ __device__ __forceinline__ f32x4_t mfma_f32_tile(const float* a, f32x4_t b, f32x
   return acc;
 }
 
+// e^x, the whole part of its exponent to base 2 taken off first (an fp32 argument of 8 is off by 2^-22, and so its power).
+__device__ __forceinline__ float exp_f64(double x) {
+  const double a = x * 1.4426950408889634, n = __builtin_rint(a);
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f(static_cast<float>(a - n)), static_cast<int>(fmax(n, -1000.0)));
+}
+
 // Block column J of T; sM holds M below the diagonal and the T_ii on it.
 template <int J> __device__ __forceinline__ void prep_column(float* sM, int lr, int lq) {
   f32x4_t t[4];
@@ -118,14 +124,18 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
     }
     if (w == 0) {
       const bool live = lane < nt;
-      float step = 0.0f, b = 0.0f;
+      double step = 0.0;
+      float b = 0.0f;
       if (live) {
         const float raw = load_elem<BF16>(p.delta, (tok + lane) * p.H + h) + (p.bias ? p.bias[h] : 0.0f);
-        step = p.softplus ? softplus_f(raw) : raw;
+        // The gradient of A is a sum over all tokens of terms of either sign, and all of them move with the steps: an
+        // fp32 softplus that is 7e-8 too large on average shows in it.
+        step = !p.softplus ? raw : BWD ? fmax(static_cast<double>(raw), 0.0) + log1p(exp(-fabs(static_cast<double>(raw))))
+                                       : softplus_f(raw);
         const float braw = load_elem<BF16>(p.beta, (tok + lane) * p.H + h);
         b = p.sigmoid ? sigmoid_f(braw) : braw;
       }
-      double cs = static_cast<double>(step) * static_cast<double>(p.A[h]);
+      double cs = step * static_cast<double>(p.A[h]);
       cs = live ? cs : 0.0;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -138,9 +148,9 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
       sClo[lane] = static_cast<float>(cs - static_cast<double>(chi));
       sBeta[lane] = b;
       float* img = reinterpret_cast<float*>(p.img + id * IMG + GATES);
-      const float grow = __builtin_amdgcn_exp2f(chi * kLog2e);
+      const float grow = exp_f64(cs);
       img[lane] = grow;
-      const float left = __builtin_amdgcn_exp2f(static_cast<float>(end - cs) * kLog2e);
+      const float left = exp_f64(end - cs);
       if constexpr (BWD) {
         img[64 + lane] = p.scale * grow;
         img[128 + lane] = left;

@@ -108,9 +108,9 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
   const int yrow = (lr * rowe32 + 4 * lq) * 2;
 
   // ---- the scale of the values and the state.  KEEP: one of the whole unit, from the largest value of each chunk.  The
-  // forward: this tile's own, from the first chunk and the initial state; a chunk with values 512 times larger than the
-  // scale was made for gets a new one (`limit`), to which the state goes over.  (Looking for the largest value before the
-  // walk, as the backward does, read all of v once more: 50 us of 380 at 16384 tokens of 40 heads.)
+  // forward: this tile's own, from the first chunk and the initial state; a chunk whose values leave [0, 1024) in that
+  // scale (`limit`) gets a new one, to which the state goes over.  (Looking for the largest value before the walk, as the
+  // backward does, would read all of v once more: 15 us of 380 at 16384 tokens of 40 heads.)
   float sc = 1.0f, inv = 1.0f, yscale = p.scale;
   unsigned limit = 0u;  // what |v| may be (fp32 bits)
   bool over = false;    // the next chunk has larger ones
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     sc = to;
     inv = 1.0f / sc;
     yscale = p.scale * inv;
-    limit = __float_as_uint(512.0f * inv);
+    limit = __float_as_uint(1024.0f * inv);
   };
   if constexpr (KEEP) {
     unsigned top = 0u;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
 #pragma unroll
   for (int d = 0; d < DT; ++d) {
     S[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.h0 && col < p.P) S[d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * d) * sc;
+    if (p.h0 && col < p.P) S[d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * d) * (KEEP ? sc * kBwdStateUp : sc);
   }
 
   // ---- chunk loads, one chunk ahead in registers
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(S[d][r]) & 0x7fffffffu);
       top = wave_max(top);
-      set_scale(top == 0u ? 0x1p60f : unit_scale(top, 1));  // nothing yet: the first value sets it
+      set_scale(top == 0u ? 0x1p60f : unit_scale(top, 5));  // nothing yet: the first value sets it
       over = false;
 #pragma unroll
       for (int d = 0; d < DT; ++d) S[d] *= sc;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
         read_step(j + 3);
       else
         read_t(j + 3 - STEPS);
-      if (kk == KT - 1) grow[t & 1] = img_vec(GATES, t);
+      if (kk == KT - 1) grow[t & 1] = img_vec(GATES, t) * (KEEP ? 1.0f / kBwdStateUp : 1.0f);
       __builtin_amdgcn_sched_barrier(0);
       if (kk == 0) x[t] = o[t] = zero;
       x[t] = mfma_f16(kf[j & 3], Sl[kk], x[t]);
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       left[t] = img_vec(KEEP ? GATES + 512 : kImgLeft, t);
-      if constexpr (KEEP) left[t] *= img_vec(GATES + 768, t);
+      if constexpr (KEEP) left[t] *= img_vec(GATES + 768, t) * kBwdStateUp;
     }
     f16x8_t kc[DT];  // K^T, a half of the tokens at a time
 #pragma unroll
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       const float a1 = (odd ? dots[3] : dots[2]) + __shfl_xor(odd ? dots[2] : dots[3], 16, 64);
       const float dot = (high ? a1 : a0) + __shfl_xor(high ? a0 : a1, 32, 64);
       rkeep = os.take(1);
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot * og[0] * inv), rkeep, lane * 4 + (col < p.P ? 0 : kPastEnd),
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot * og[0] * (inv / kBwdStateUp)), rkeep, lane * 4 + (col < p.P ? 0 : kPastEnd),
                                             0, 0);
     } else {
       // ---- Y^T = ((Q S0)^T diag(e^cs) + R^T P^T) scale
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
         const unsigned top = wave_max(staged_top());
         if (over && top < 0x7f800000u) {
           const float was = inv;
-          set_scale(unit_scale(top, 1));
+          set_scale(unit_scale(top, 5));
           by *= sc * was;
         }
         over = false;
