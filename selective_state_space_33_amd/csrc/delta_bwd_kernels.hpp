@@ -334,7 +334,7 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
         e0 = mfma_f16(Sl[kk], s0[kk], e0);
         e1 = mfma_f16(Sh[kk], s0[kk], e1);
         e0 = mfma_f16(Sh[kk], s0[KT + kk], e0);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Sh[kk]), ra, mine, kk * kFrag, 0);
+        store_b128(__builtin_bit_cast(u32x4_t, Sh[kk]), ra, mine + kk * kFrag);
       }
       if constexpr (j / KT == 3) load_s0(kk);
       if constexpr (kk == KT - 1 && j + 1 < STEPS) finish(t);
@@ -389,8 +389,8 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     // dV of two tiles: kept as a pair, times -e^cs as the next product's operand; e^cs (S0 k) . dv of its tokens
     auto take_dv = [&](int m) {
       split_f16(u[2 * m], u[2 * m + 1], Nh, Nl);
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Nh), rv, mine, m * kFrag, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Nl), rv, mine, (2 + m) * kFrag, 0);
+      store_b128(__builtin_bit_cast(u32x4_t, Nh), rv, mine + m * kFrag);
+      store_b128(__builtin_bit_cast(u32x4_t, Nl), rv, mine + (2 + m) * kFrag);
       const f32x4_t v0 = u[2 * m] * -grow[2 * m], v1 = u[2 * m + 1] * -grow[2 * m + 1];
       split_f16(v0, v1, Vh[m], Vl[m]);
       gt[2 * m] = v0 * z[2 * m], gt[2 * m + 1] = v1 * z[2 * m + 1];
@@ -835,8 +835,8 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
   for (int i = 0; i < KPER; ++i) {
     const int e = tid + 256 * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
     const int off = static_cast<int>((row * krow + cc) * 2);
-    __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4_t*>(&lds.out[0][row * CL + cc]), oq, off, 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4_t*>(&lds.out[1][row * CL + cc]), ok, off, 0, 0);
+    store_b128(*reinterpret_cast<const u32x4_t*>(&lds.out[0][row * CL + cc]), oq, off);
+    store_b128(*reinterpret_cast<const u32x4_t*>(&lds.out[1][row * CL + cc]), ok, off);
   }
 }
 

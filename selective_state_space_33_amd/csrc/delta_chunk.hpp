@@ -143,6 +143,13 @@ template <int DK> __device__ __forceinline__ f16x8_t lds_col_frag(const uint16_t
   return __builtin_bit_cast(f16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
 }
 
+// A 16-byte buffer store.  The whole offset goes into the lane's: with a scalar register for a part of it the compiler
+// takes such a store as done with its data at once, and let the next instruction overwrite them; on the MI355X four
+// lanes of every sixteen then stored the new value of the first dword, now and then.
+__device__ __forceinline__ void store_b128(u32x4_t v, rsrc_t r, int voff) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, 0, 0);
+}
+
 // f(IC<0>) .. f(IC<N - 1>): a loop whose index is a constant in the body.
 template <class F, int... I> __device__ __forceinline__ void static_for_each(F&& f, std::integer_sequence<int, I...>) {
   (f(IC<I>{}), ...);

@@ -341,8 +341,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       // (S0 q) . dy goes into the gradient of a fade, which needs both parts of S0
       if constexpr (KEEP) o[t] = mfma_f16(Sl[kk], qf[j & 3], o[t]);
       if constexpr (KEEP && j < 2 * KT)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, j < KT ? Sh[j] : Sl[j - KT]), rkeep, mine,
-                                               j * kFrag, 0);
+        store_b128(__builtin_bit_cast(u32x4_t, j < KT ? Sh[j] : Sl[j - KT]), rkeep, mine + j * kFrag);
       if constexpr (kk == 0 && t > 0) finish_x(t - 1);
       // the state itself (its operands are copies) fades here, out of the chain
 #pragma unroll
@@ -443,8 +442,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         split_f16(u[2 * m], u[2 * m + 1], Rf[m], Rl);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Rf[m]), rkeep, mine, m * kFrag, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, Rl), rkeep, mine, (2 + m) * kFrag, 0);
+        store_b128(__builtin_bit_cast(u32x4_t, Rf[m]), rkeep, mine + m * kFrag);
+        store_b128(__builtin_bit_cast(u32x4_t, Rl), rkeep, mine + (2 + m) * kFrag);
       }
       og[0] = *reinterpret_cast<const float*>(&b.img[GATES + 256 + lane * 4]);
     } else {

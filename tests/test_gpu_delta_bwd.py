@@ -192,3 +192,24 @@ def test_backward_of_wide_heads_pulling_one_way():
     x = I.random_delta_inputs(rng, 1, 70, 1, 1, 32, 1040)
     x["v"] = np.full(x["v"].shape, 1.9375, np.float32)
     check(x, "wide", dy=np.full(x["v"].shape, 0.96875, np.float32))
+
+
+@pytest.mark.parametrize("N,P,H", [(32, 192, 24), (64, 64, 48), (96, 80, 40), (128, 128, 40)])
+def test_backward_of_more_workgroups_than_the_chip_holds(N, P, H):
+    """Results of a call that takes several rounds of workgroups, in a workspace full of NaN: finite, and the same again."""
+    rng = np.random.default_rng(3800 + N)
+    B, L, G = 8, 300, H // 2
+    say(f"delta bwd rounds N={N} P={P}")
+    x = I.random_delta_inputs(rng, B, L, G, H, N, P)
+    t = tensors(x, "bf16")
+    dy, h0 = dev(rng.standard_normal(x["v"].shape), "bf16"), dev(0.3 * rng.standard_normal((B, H, P, N)))
+    size = ops.ssm_delta_bwd_workspace_size(B, L, H, P, G, N, 0, torch.bfloat16)
+    runs = []
+    for _ in range(3):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda:0")
+        runs.append(ops.ssm_delta_bwd(t["q"], t["k"], t["v"], t["delta"], t["A"], t["beta"], dy,
+                                      delta_bias=t["delta_bias"], initial_state=h0, workspace=ws))
+        torch.cuda.synchronize()
+    for n, a in runs[0].items():
+        assert torch.isfinite(a.float()).all(), n
+        assert all(torch.equal(a, r[n]) for r in runs[1:]), n
