@@ -25,9 +25,9 @@
 // forward's holds S, writes dV and keeps it and dS; delta_grad_kernel forms dq,
 // dk, db and dla of all chunks at once, a workgroup per chunk and key head,
 // which sums its heads in order.  2 x 4096 tokens of 40 heads of 128 channels,
-// dstate 128: 80, 270, 352 and 300 us.  The walks are bound by their chunks'
-// chain (64 chunks, 4.2 and 5.5 us each, 160 of the 256 CUs), the last by
-// latency at two workgroups a CU (740 MB, 2.5 TB/s).
+// dstate 128: 86, 280, 365 and 305 us.  The walks are bound by their chunks'
+// chain (64 chunks, 4.4 and 5.7 us each, 160 of the 256 CUs), the last by
+// latency at two workgroups a CU (740 MB, 2.4 TB/s).
 //
 // Precision.  What goes from chunk to chunk, dV and every term of dla is a pair
 // of fp16 (22 bits) in fp32 accumulators.  dY and what is linear in it may have

@@ -7,7 +7,7 @@
 // fp32 sums), of Q each wavefront keeps one row tile in registers; it forms a
 // row of M tiles and a column of P tiles, five in all, then M takes K's place
 // (18 KB a workgroup: six of them share a CU, which hides their serial parts;
-// with Q in LDS too, 35 KB and four, it took 115 us where it takes 94: 16384
+// with Q in LDS too, 35 KB and four, it took 115 us where it takes 100: 16384
 // tokens of 40 heads, dstate 128, 360 MB).  cs is summed in fp64 and kept
 // as a pair of floats: differences of neighbours deep in a fast-fading chunk
 // would otherwise lose bits.  The inverse is a forward substitution: the four
