@@ -244,7 +244,8 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     };
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
     constexpr int STEPS = 4 * KT;
-    auto tile_of = [](int j) { return (j / KT + 2) & 3; };  // tokens' tiles in the order 2, 3, 0, 1: T^T takes the last two first
+    // tokens' tiles in the order 2, 3, 0, 1: T^T takes the last two first
+    auto tile_of = [](int j) { return (j / KT + 2) & 3; };
     f16x8_t kf[4];
     auto read_step = [&](int j) { kf[j & 3] = plain_row_frag<CL>(b.k, 16 * tile_of(j) + lr, j % KT, lq); };
     u32x2_t tq[4];
@@ -304,9 +305,10 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
       const int m = t >> 1;
       const f32x4_t lx = x[t] * left;
       const f16x8_t hi = r0[m], lo = r0[2 + m];
-      const f16x4_t hs = t & 1 ? __builtin_shufflevector(hi, hi, 4, 5, 6, 7) : __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
-      const f16x4_t ls4 = t & 1 ? __builtin_shufflevector(lo, lo, 4, 5, 6, 7) : __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
-      lt[t] = fma_pair(lx * beta, hs, ls4, zero);
+      lt[t] = t & 1 ? fma_pair(lx * beta, __builtin_shufflevector(hi, hi, 4, 5, 6, 7),
+                               __builtin_shufflevector(lo, lo, 4, 5, 6, 7), zero)
+                    : fma_pair(lx * beta, __builtin_shufflevector(hi, hi, 0, 1, 2, 3),
+                               __builtin_shufflevector(lo, lo, 0, 1, 2, 3), zero);
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[t][r] = beta[r] * __builtin_fmaf(wy[t][r], 1.0f / kBwdPScale, lx[r]);
       if (t & 1) {
@@ -427,7 +429,8 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     e0 += e1;  // its diagonal: each channel's <dS, S0>
     const float diag = (lr & 2) ? ((lr & 1) ? e0[3] : e0[2]) : ((lr & 1) ? e0[1] : e0[0]);
     rt = es.take(true);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lq == (lr >> 2) ? diag * fade * state : 0.0f), rt, mine4, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lq == (lr >> 2) ? diag * fade * state : 0.0f), rt, mine4, 0,
+                                          0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       vt[t] *= inv;
@@ -489,7 +492,8 @@ template <int DK> __global__ void __launch_bounds__(256, 2) delta_grad_kernel(De
   uint16_t *const sK = lds.k, *const sQ = lds.q;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 15, lq = lane >> 4;
-  const unsigned groups = static_cast<unsigned>(p.G), id = xcd_order(blockIdx.x, static_cast<unsigned>(p.slots) * groups);
+  const unsigned groups = static_cast<unsigned>(p.G);
+  const unsigned id = xcd_order(blockIdx.x, static_cast<unsigned>(p.slots) * groups);
   const int64_t slot = id / groups, g = id % groups, rep = static_cast<unsigned>(p.H) / groups;
   int64_t s = 0;
   if (p.cu) {

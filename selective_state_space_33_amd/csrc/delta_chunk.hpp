@@ -198,8 +198,9 @@ __device__ __forceinline__ int64_t delta_slot_seq(const int64_t* cu, int64_t n, 
 // What is linear in the values (or in the gradients) may have any magnitude, but passes through fp16 pairs.  So values
 // and initial states are scaled by the power of two that brings their largest magnitude to [32, 64) (the backward's to
 // [2, 4)), dY and dfinal to [16, 32), and results scaled back, all exactly.  (Above, states and sums have room up to the
-// largest fp16, 65504; the lo part of a pair, whose last place is 2^-24, keeps its bits down to 2^-3.)  The scale is 1 where nothing, or something
-// not finite, is the largest; it stays between 2^-60 and 2^60, so that products of two stay in fp32.
+// largest fp16, 65504; the lo part of a pair, whose last place is 2^-24, keeps its bits down to 2^-3.)  The scale is 1
+// where nothing, or something not finite, is the largest; it stays between 2^-60 and 2^60, so that products of two stay
+// in fp32.
 __device__ __forceinline__ float unit_scale(unsigned amax_bits, int target) {
   const int e = static_cast<int>(amax_bits >> 23) - 127;
   if (amax_bits == 0u || e > 127) return 1.0f;

@@ -42,7 +42,9 @@ inline int64_t delta_slots(int64_t batch, int64_t L, int64_t nseq) {
 }
 // A workspace starts with a header; the order of packed sequences follows.
 constexpr size_t kDeltaHeader = 256;
-inline size_t delta_order_bytes(int64_t nseq) { return (static_cast<size_t>(nseq) * 4 + 255) & ~static_cast<size_t>(255); }
+inline size_t delta_order_bytes(int64_t nseq) {
+  return (static_cast<size_t>(nseq) * 4 + 255) & ~static_cast<size_t>(255);
+}
 
 inline ssm_status_t check_delta_args(const DeltaArgs& a, const void* y, const float* final_state) {
   if (!a.q || !a.k || !a.v || !a.delta || !a.A || !a.beta || !y) return SSM_ERR_INVALID_ARG;

@@ -71,7 +71,8 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
   const int lr = lane & 15, lq = lane >> 4;
   if (p.words && blockIdx.x == 0 && tid < 4) p.words[tid] = 0u;
   if (tid == 0) sTop = 0u;
-  const unsigned heads = static_cast<unsigned>(p.H), id32 = xcd_order(blockIdx.x, static_cast<unsigned>(p.slots) * heads);
+  const unsigned heads = static_cast<unsigned>(p.H);
+  const unsigned id32 = xcd_order(blockIdx.x, static_cast<unsigned>(p.slots) * heads);
   const int64_t id = id32, slot = id32 / heads, h = id32 % heads, g = key_head(h, p.H, p.G);
   // the sequence of this slot: the last one that starts at or before it
   int64_t s = 0;

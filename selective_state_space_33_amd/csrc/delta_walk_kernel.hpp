@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
 #pragma unroll
   for (int d = 0; d < DT; ++d) {
     S[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.h0 && col < p.P) S[d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * d) * (KEEP ? sc * kBwdStateUp : sc);
+    if (p.h0 && col < p.P)
+      S[d] = *reinterpret_cast<const f32x4_t*>(p.h0 + sbase + 16 * d) * (KEEP ? sc * kBwdStateUp : sc);
   }
 
   // ---- chunk loads, one chunk ahead in registers
@@ -482,8 +483,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       const float a1 = (odd ? dots[3] : dots[2]) + __shfl_xor(odd ? dots[2] : dots[3], 16, 64);
       const float dot = (high ? a1 : a0) + __shfl_xor(high ? a0 : a1, 32, 64);
       rkeep = os.take(1);
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot * og[0] * (inv / kBwdStateUp)), rkeep, lane * 4 + (col < p.P ? 0 : kPastEnd),
-                                            0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot * og[0] * (inv / kBwdStateUp)), rkeep,
+                                            lane * 4 + (col < p.P ? 0 : kPastEnd), 0, 0);
     } else {
       // ---- Y^T = ((Q S0)^T diag(e^cs) + R^T P^T) scale
 #pragma unroll

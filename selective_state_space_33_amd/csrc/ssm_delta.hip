@@ -94,8 +94,8 @@ template <int DK> hipError_t run_chunked(DeltaChunkParams& p, hipStream_t s) {
   // 282 us, 4 rows 484 / 346, 8 rows 767 / 661.
   const int64_t small = units * ((tiles + 3) / 4);
   if (tiles > 4 && small > device_cu_count())
-    hipLaunchKernelGGL((delta_walk_kernel<DK, 8, false>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))), dim3(512),
-                       0, s, p);
+    hipLaunchKernelGGL((delta_walk_kernel<DK, 8, false>), dim3(static_cast<unsigned>(units * ((tiles + 7) / 8))),
+                       dim3(512), 0, s, p);
   else
     hipLaunchKernelGGL((delta_walk_kernel<DK, 4, false>), dim3(static_cast<unsigned>(small)), dim3(256), 0, s, p);
   return hipGetLastError();

@@ -20,7 +20,8 @@ bool bwd_supported(int64_t batch, int64_t L, int64_t heads, int64_t headdim, int
   return delta_slots(batch, L, nseq) <= 0x7fffffffLL / heads;
 }
 
-// The workspace: [header][order of packed sequences][largest gradients, values' scales, largest values][images][S0][dS][R][dV][the terms of dla][edges][parts of dA, dbias].
+// The workspace: [header][order of packed sequences][largest gradients, values' scales, largest values][images][S0][dS]
+// [R][dV][the terms of dla][edges][parts of dA, dbias].
 struct BwdLayout {
   size_t order, amax, vscale, vmax, img, state, adj, r, dvh, oterm, gterm, lterm, edge, part, total;
 };
