@@ -30,7 +30,7 @@ inline bool delta_sizes_ok(int64_t batch, int64_t L, int64_t heads, int64_t head
 // States of 32 .. 128 in steps of 32, and 192 and 256; sizes whose products stay far below 2^63.
 inline bool delta_shape_supported(int64_t batch, int64_t L, int64_t heads, int64_t headdim, int64_t dstate) {
   if (dstate % 32 != 0 || dstate > 256 || dstate == 160 || dstate == 224) return false;
-  if (batch > (1LL << 31) || L > (1LL << 31) || heads > (1 << 20) || headdim > (1 << 20)) return false;
+  if (batch > (1LL << 31) || L > 0x7fffffffLL || heads > (1 << 20) || headdim > (1 << 20)) return false;
   // one workgroup per 32 or more rows of a (row, head) unit: the grid stays below 2^31
   return batch * heads <= 0x7fffffffLL / ((headdim + 31) / 32);
 }

@@ -35,7 +35,7 @@ __device__ __forceinline__ f32x4_t mfma_f32_tile(const float* a, f32x4_t b, f32x
 // e^x, the whole part of its exponent to base 2 taken off first (an fp32 argument of 8 is off by 2^-22, and so its power).
 __device__ __forceinline__ float exp_f64(double x) {
   const double a = x * 1.4426950408889634, n = __builtin_rint(a);
-  return __builtin_ldexpf(__builtin_amdgcn_exp2f(static_cast<float>(a - n)), static_cast<int>(fmax(n, -1000.0)));
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f(static_cast<float>(a - n)), static_cast<int>(fmin(fmax(n, -1000.0), 1000.0)));
 }
 
 // Block column J of T; sM holds M below the diagonal and the T_ii on it.

@@ -48,6 +48,7 @@ __device__ __forceinline__ unsigned max_bf16x2(unsigned a, unsigned b) {
   return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a & 0x7fff7fffu),
                                                                 __builtin_bit_cast(u16x2_t, b & 0x7fff7fffu)));
 }
+__device__ __forceinline__ unsigned finite_bits(unsigned v) { return v < 0x7f800000u ? v : 0u; }
 __device__ __forceinline__ unsigned wave_max(unsigned v) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) v = max(v, static_cast<unsigned>(__shfl_xor(static_cast<int>(v), o, 64)));
@@ -184,7 +185,8 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     constexpr int i = decltype(item)::value;
     if constexpr (i < PER) {
       const int e = tid + NTH * i;
-      const int off = (e / (DK / 8)) * krow32 * 2 + (e % (DK / 8)) * 16;
+      // (a piece behind the 64 rows has no place: it is not read either, the tensor may end before it)
+      const int off = PIECES % NTH == 0 || e < PIECES ? (e / (DK / 8)) * krow32 * 2 + (e % (DK / 8)) * 16 : kPastEnd;
       gk[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, off, 0, 0));
       gq[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq, off, 0, 0));
     } else if constexpr (i < PER + IPER) {
@@ -204,7 +206,6 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     constexpr int i = decltype(item)::value;
     if constexpr (i < PER) {
       const int e = tid + NTH * i, row = e / (DK / 8), cc = (e % (DK / 8)) * 8;
-      // (a piece behind the 64 rows was loaded as zero and has no place)
       if (PIECES % NTH == 0 || e < PIECES) {
         const u32x4_t k8 = bf16x8_as_f16(gk[i]), q8 = bf16x8_as_f16(gq[i]);
         lds_store_paired(&b.k[row * kRowLd<DK>], cc, k8);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     }
   };
 
-  // the largest |v| of the chunk that this wavefront has staged last
+  // the largest finite |v| of the chunk that this wavefront has staged last
   auto staged_top = [&] {
     int own = threadIdx.x;  // (opaque: what only this needs is not carried through the loop)
     asm volatile("" : "+v"(own));
@@ -238,9 +239,11 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const u32x2_t v = *reinterpret_cast<const u32x2_t*>(a + 256 * t);
-      m = max_bf16x2(m, max_bf16x2(v[0], v[1]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        m = max(m, max(finite_bits(v[i] & 0x7fff0000u), finite_bits((v[i] << 16) & 0x7fff0000u)));
     }
-    return max(m & 0x7fff0000u, m << 16);
+    return m;
   };
 
   if (nchunks > 0) {
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(S[d][r]) & 0x7fffffffu);
+        for (int r = 0; r < 4; ++r) top = max(top, finite_bits(__float_as_uint(S[d][r]) & 0x7fffffffu));
       top = wave_max(top);
       set_scale(top == 0u ? 0x1p60f : unit_scale(top, 5));  // nothing yet: the first value sets it
       over = false;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
         asm volatile("" : "+v"(own));
         float by = broken && lds_first[w][own] < kDeltaC ? __builtin_nanf("") : 1.0f;
         const unsigned top = wave_max(staged_top());
-        if (over && top < 0x7f800000u) {
+        if (__uint_as_float(top) > __uint_as_float(limit)) {
           const float was = inv;
           set_scale(unit_scale(top, 5));
           by *= sc * was;

@@ -84,7 +84,6 @@ bool delta_chunked(int64_t L, int64_t heads, int64_t headdim, int64_t dstate, in
 }
 template <int DK> hipError_t run_chunked(DeltaChunkParams& p, hipStream_t s) {
   const int64_t grid = p.slots * p.H;
-  if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
   hipLaunchKernelGGL((delta_prep_kernel<DK, false>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -132,6 +131,7 @@ extern "C" size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t
   if ((nseq > 0 && batch != 1) || nseq < 0) return 0;
   if (!delta_shape_supported(nseq > 0 ? nseq : batch, L, heads, headdim, dstate)) return 0;
   if (!delta_chunked(L, heads, headdim, dstate, nseq, dt)) return 0;
+  if (delta_slots(batch, L, nseq) > 0x7fffffffLL / heads) return 0;
   return kDeltaHeader + delta_order_bytes(nseq) + static_cast<size_t>(delta_slots(batch, L, nseq)) * heads * kImgBytes;
 }
 
@@ -156,6 +156,7 @@ extern "C" ssm_status_t ssm_delta_fwd(const void* q, const void* k, const void* 
                                              : run_step<BF16>(p, units, dstate, stream);
     return e == hipSuccess ? SSM_OK : SSM_ERR_HIP;
   }
+  if (delta_slots(batch, L, nseq) > 0x7fffffffLL / heads) return SSM_ERR_UNSUPPORTED;  // a workgroup for each
   const size_t need = ssm_delta_fwd_workspace_size(batch, L, heads, headdim, ngroups, dstate, nseq, dt);
   if (!workspace || workspace_bytes < need || !delta_aligned(workspace, 256)) return SSM_ERR_INVALID_ARG;
   DeltaChunkParams p = {};

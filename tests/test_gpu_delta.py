@@ -346,3 +346,45 @@ def test_garbage_in_padding_leaves_what_is_before_it(where, token, value):
     assert bool(same.all())
     if where == "k" or (where in ("delta", "beta") and np.isnan(value)):
         assert not torch.isfinite(s[1, heads]).any()
+
+
+@pytest.mark.parametrize("N,P", [(32, 80), (96, 80), (64, 144), (128, 96)])
+@pytest.mark.parametrize("L", [65, 130])
+def test_wide_workgroups_give_what_narrow_ones_do(N, P, L):
+    """A batch large enough for eight wavefronts a workgroup, its last row ending where its tensors do, one token into a
+    chunk: each row as alone, where the workgroups have four, bit for bit."""
+    rng = np.random.default_rng(1630 + N)
+    B, H = 16, 24
+    x = I.random_delta_inputs(rng, B, L, H // 2, H, N, P)
+    say(f"delta wide N={N} P={P} L={L}")
+    t = tensors(x, "bf16")
+    h0 = dev(rng.standard_normal((B, H, P, N)))
+
+    def call(s):
+        return ops.ssm_delta_fwd(*(t[n][s].contiguous() for n in ("q", "k", "v", "delta")), t["A"],
+                                 t["beta"][s].contiguous(), delta_bias=t["delta_bias"], initial_state=h0[s].contiguous())
+
+    y, S = call(slice(0, B))
+    for b in (0, 7, B - 1):
+        yb, Sb = call(slice(b, b + 1))
+        assert torch.equal(y[b:b + 1], yb) and torch.equal(S[b:b + 1], Sb), b
+
+
+def test_values_that_outgrow_their_scale_beside_a_nan():
+    """From the second chunk on the values are a million times larger, and one of them a NaN: its channel is lost, the
+    others of its tile are those of the clean call."""
+    rng = np.random.default_rng(1640)
+    x = I.random_delta_inputs(rng, 1, 200, 1, 2, 64, 32)
+    x["v"][:, :64] = I.round_to_bf16((x["v"][:, :64] * 1e-6).astype(np.float32))
+    x["v"][0, 70, 1, 5] = 0.25
+    say("delta NaN where the scale changes")
+    y0, s0 = run(x, "bf16")
+    yo, so = D.delta_fwd(**x)
+    M, Ms = D.delta_magnitudes(**x)
+    ey, _ = y_off(host(y0), yo, M, "bf16")
+    assert ey <= 1 and s_off(host(s0), so, Ms) <= TOL_STATE
+    x["v"][0, 70, 1, 5] = np.nan
+    y, s = run(x, "bf16")
+    assert not torch.isfinite(y[0, 70:, 1, 5]).any() and not torch.isfinite(s[0, 1, 5]).any()
+    y[0, 70:, 1, 5], s[0, 1, 5] = y0[0, 70:, 1, 5], s0[0, 1, 5]
+    assert torch.equal(y, y0) and torch.equal(s, s0)
