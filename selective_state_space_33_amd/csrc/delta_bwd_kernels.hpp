@@ -390,6 +390,7 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     f32x4_t gt[4];
     // dV of two tiles: kept as a pair, times -e^cs as the next product's operand; e^cs (S0 k) . dv of its tokens
     auto take_dv = [&](int m) {
+      u[2 * m] *= 1.0f / kBwdTUp, u[2 * m + 1] *= 1.0f / kBwdTUp;
       split_f16(u[2 * m], u[2 * m + 1], Nh, Nl);
       store_b128(__builtin_bit_cast(u32x4_t, Nh), rv, mine + m * kFrag);
       store_b128(__builtin_bit_cast(u32x4_t, Nl), rv, mine + (2 + m) * kFrag);
@@ -433,7 +434,7 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
                                           0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      vt[t] *= inv;
+      vt[t] *= inv / kBwdTUp;
       yo[t] = u32x2_t{pack_bf16x2(vt[t][0], vt[t][1]), pack_bf16x2(vt[t][2], vt[t][3])};
     }
     split_f16(S[DT - 2], S[DT - 1], Sh[KT - 1], Sl[KT - 1]);

@@ -55,6 +55,10 @@ constexpr float kBwdPScale = 16.0f;          // P is kept 16 times as large, awa
 // the values that make them, and the last place of a pair's lo part is 2^-24 (states of 128 x 128 were off by 3.5e-7
 // without it, by 2.2e-7 with it).
 constexpr float kBwdStateUp = 32.0f;
+// T too, whose elements off the diagonal are small, and X (3 x 333 tokens: the gradient of A up to 1.6e-6 off without,
+// 3.6e-7 with them).
+constexpr float kBwdTUp = 64.0f;
+constexpr float kBwdXUp = 16.0f;
 constexpr int kBwdBack = 12 * kFrag;         // T^T hi, T^T lo, P^T hi, P^T lo: six fragments each
 constexpr int kBwdGates = kBwdBack + 24 * kFrag;
 // (64 floats each: e^{cs_t}, scale e^{cs_t}, e^{cs_C - cs_t}, b_t, and cs_t as a pair hi, lo)

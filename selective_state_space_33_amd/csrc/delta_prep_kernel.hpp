@@ -318,8 +318,9 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
     };
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
     const f32x4_t x0 = block(2 * m), x1 = 2 * m + 1 <= t ? block(2 * m + 1) : zero;
+    constexpr float up = BWD ? kBwdTUp : 1.0f;
     f16x8_t hi, lo;
-    split_f16(x0, x1, hi, lo);
+    split_f16(x0 * up, x1 * up, hi, lo);
     char* out = p.img + id * IMG + f * kFrag + ln * 16;
     *reinterpret_cast<f16x8_t*>(out + kImgThi) = hi;
     *reinterpret_cast<f16x8_t*>(out + kImgTlo) = lo;
@@ -334,7 +335,8 @@ template <int DK, bool BWD> __global__ void __launch_bounds__(256) delta_prep_ke
       for (int u = 0; u < 2; ++u) {
         const int t = 2 * m + u;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) half[u][r] = t < j ? 0.0f : sM[(16 * j + q4 + r) * kPrepLd + 16 * t + row];
+        for (int r = 0; r < 4; ++r)
+          half[u][r] = t < j ? 0.0f : sM[(16 * j + q4 + r) * kPrepLd + 16 * t + row] * kBwdTUp;
       }
       f16x8_t hi, lo;
       split_f16(half[0], half[1], hi, lo);

@@ -324,10 +324,11 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
     };
     f32x4_t x[4], o[4], grow[2];
     f16x8_t Xh[2], Xl[2];
+    const float vsc = KEEP ? sc * kBwdXUp : sc;
     auto finish_x = [&](int t) {
       const float v[4] = {bf16_lo(vq[t][0]), bf16_hi(vq[t][0]), bf16_lo(vq[t][1]), bf16_hi(vq[t][1])};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(-grow[t & 1][r], x[t][r], v[r] * sc);
+      for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(-grow[t & 1][r], x[t][r], v[r] * vsc);
       if (t & 1) split_f16(x[t - 1], x[t], Xh[t >> 1], Xl[t >> 1]);
     };
     static_for<STEPS>([&](auto step) {
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
         read_step(j + 3);
       else
         read_t(j + 3 - STEPS);
-      if (kk == KT - 1) grow[t & 1] = img_vec(GATES, t) * (KEEP ? 1.0f / kBwdStateUp : 1.0f);
+      if (kk == KT - 1) grow[t & 1] = img_vec(GATES, t) * (KEEP ? kBwdXUp / kBwdStateUp : 1.0f);
       __builtin_amdgcn_sched_barrier(0);
       if (kk == 0) x[t] = o[t] = zero;
       x[t] = mfma_f16(kf[j & 3], Sl[kk], x[t]);
@@ -422,6 +423,10 @@ __global__ void __launch_bounds__(64 * W) delta_walk_kernel(typename DeltaWalkAr
       t_product(2, 1, i.value);
       t_product(3, 1, i.value);
     });
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] *= 1.0f / (kBwdXUp * kBwdTUp);
+    }
     split_f16(u[0] * left[0], u[1] * left[1], Uh[0], Ul[0]);
     auto state_product = [&](int d, int m) {
       S[d] = mfma_f16(kc[d], Uh[m], S[d]);
