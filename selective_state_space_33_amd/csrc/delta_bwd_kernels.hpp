@@ -25,8 +25,8 @@
 // forward's holds S, writes dV and keeps it and dS; delta_grad_kernel forms dq,
 // dk, db and dla of all chunks at once, a workgroup per chunk and key head,
 // which sums its heads in order.  2 x 4096 tokens of 40 heads of 128 channels,
-// dstate 128: 86, 280, 365 and 305 us.  The walks are bound by their chunks'
-// chain (64 chunks, 4.4 and 5.7 us each, 160 of the 256 CUs), the last by
+// dstate 128: 86, 277, 350 and 304 us.  The walks are bound by their chunks'
+// chain (64 chunks, 4.3 and 5.5 us each, 160 of the 256 CUs), the last by
 // latency at two workgroups a CU (740 MB, 2.4 TB/s).
 //
 // Precision.  What goes from chunk to chunk, dV and every term of dla is a pair
@@ -340,8 +340,6 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
       }
       if constexpr (j / KT == 3) load_s0(kk);
       if constexpr (kk == KT - 1 && j + 1 < STEPS) finish(t);
-#pragma unroll
-      for (int d = j * DT / STEPS; d < (j + 1) * DT / STEPS; ++d) S[d] *= fade;
       slot(IC<j>{});
     });
     // ---- dV = T^T (b Y0): the last two tiles' share of it while the rest of b Y0 is finished, Q^T dY between
@@ -371,11 +369,20 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     t_products(0, 1);
     t_products(1, 1);
     __builtin_amdgcn_sched_barrier(0);
+    // What the chunk adds to dS, summed apart and added at the end: the products round at the size of what they add
+    // (363 us so far, 350 now).
+    f32x4_t more[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) more[d] = zero;
     auto state_product = [&](int d, const f16x8_t& hi, const f16x8_t& lo) {
-      S[d] = mfma_f16(cf[d], hi, S[d]);
-      S[d + 1] = mfma_f16(cf[d + 1], hi, S[d + 1]);
-      S[d] = mfma_f16(cf[d], lo, S[d]);
-      S[d + 1] = mfma_f16(cf[d + 1], lo, S[d + 1]);
+      more[d] = mfma_f16(cf[d], lo, more[d]);
+      more[d + 1] = mfma_f16(cf[d + 1], lo, more[d + 1]);
+      more[d] = mfma_f16(cf[d], hi, more[d]);
+      more[d + 1] = mfma_f16(cf[d + 1], hi, more[d + 1]);
+    };
+    auto take_more = [&](int d) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[d][r] = __builtin_fmaf(fade, S[d][r], more[d][r]);
     };
     static_for<KT>([&](auto k) {
       constexpr int d = 2 * decltype(k)::value;
@@ -419,7 +426,11 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
     static_for<KT>([&](auto k) {
       constexpr int kk = decltype(k)::value, d = 2 * kk;
       state_product(d, Vh[0], Vl[0]);
-      if constexpr (kk > 0) split_f16(S[d - 2], S[d - 1], Sh[kk - 1], Sl[kk - 1]);
+      if constexpr (kk > 0) {
+        take_more(d - 2);
+        take_more(d - 1);
+        split_f16(S[d - 2], S[d - 1], Sh[kk - 1], Sl[kk - 1]);
+      }
       slot(IC<STEPS + KT + kk>{});
     });
     // ---- the terms of dla, and dV's rows
@@ -437,6 +448,8 @@ template <int DK, int W> __global__ void __launch_bounds__(64 * W) delta_bwd_wal
       vt[t] *= inv / kBwdTUp;
       yo[t] = u32x2_t{pack_bf16x2(vt[t][0], vt[t][1]), pack_bf16x2(vt[t][2], vt[t][3])};
     }
+    take_more(DT - 2);
+    take_more(DT - 1);
     split_f16(S[DT - 2], S[DT - 1], Sh[KT - 1], Sl[KT - 1]);
     __syncthreads();
   }
