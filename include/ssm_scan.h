@@ -418,8 +418,8 @@ ssm_status_t ssm_scan_trap_bwd(const void* u, const void* delta, const float* A,
  * 2^22 and v and y 8-byte aligned run in chunks of 64 tokens on the matrix
  * cores; everything else runs token by token in fp32.  In the chunked plan q
  * and k pass through fp16 (exactly from 2^-14 to 65504 in magnitude; smaller
- * elements to a multiple of 2^-24, larger ones make what they reach inf or
- * NaN); v, the states and y may have any magnitude (they are scaled by powers
+ * elements to a multiple of 2^-24, larger ones, or products b q.k from
+ * there on, make what they reach inf or NaN); v, the states and y may have any magnitude (they are scaled by powers
  * of two), with 22 significant bits on the states' way, relative to the
  * largest value and state of 16 channels.  A token that is not finite (in
  * padding, say) reaches itself and the tokens and states behind it, never a
@@ -456,7 +456,8 @@ size_t ssm_delta_fwd_workspace_size(int64_t batch, int64_t L, int64_t heads, int
  *   headdim and heads * dstate up to 2^22; else UNSUPPORTED.  q, k, v, dy, dq,
  *   dk, dv and the states 16-byte aligned, everything else to its element.  Only
  *   dfinal_state and dinitial_state may be the same buffer; no other output
- *   may alias anything.  q and k pass through fp16 as in ssm_delta_fwd; v and
+ *   may alias anything.  q and k pass through fp16 as in ssm_delta_fwd, and
+ *   scale q.k of a chunk's tokens has to stay below 4000 in magnitude; v and
  *   the initial state, and dy and dfinal_state, may have any magnitude: each
  *   (row, head) is scaled by powers of two of its own.  An input that is not
  *   finite makes every gradient of its row (or sequence) and head unusable.
